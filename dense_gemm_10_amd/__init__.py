@@ -5,7 +5,8 @@ behind the C ABI declared in include/densegemm.h.  The functions below carry
 the ABI's names (dg_gemm, dg_gemm_workspace_size, dg_gemm_describe,
 dg_status_string, dg_version, dg_schedule_map, dg_gemm_noalloc).  ``gemm()`` is a
 convenience wrapper for torch tensors; torch is used for device memory and
-streams only.
+streams only.  The products over groups of rows and with 4-bit weights are
+bound in grouped.py and named here too.
 
 The shared library is built in-tree by ``dense_gemm_10_amd.build``; if it is
 missing, loading raises instead of falling back to anything else.
@@ -23,6 +24,9 @@ __all__ = [
     "DG_ALGO_MFMA_F32", "DG_ALGO_MFMA_F16", "DgGemmDesc", "DgError", "make_desc", "dg_version",
     "dg_status_string", "dg_gemm_workspace_size", "dg_gemm", "dg_gemm_describe",
     "dg_schedule_map", "dg_gemm_noalloc", "DG_NOALLOC_SCRATCH_BYTES", "gemm", "library_path",
+    "DG_RAGGED_M", "DG_RAGGED_K", "DgGroupedDesc", "DgQweightDesc", "make_grouped_desc",
+    "make_qweight_desc", "dg_gemm_grouped", "dg_gemm_grouped_describe", "dg_gemm_qweight",
+    "dg_gemm_qweight_describe", "gemm_grouped", "gemm_grouped_k", "gemm_qweight",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -285,3 +289,9 @@ def gemm(A, B, C=None, *, alpha=1.0, beta=0.0, bias=None, act="none", out_dtype=
             ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     dg_gemm(desc, A.data_ptr(), B.data_ptr(), C.data_ptr(), ws_ptr, ws_bytes, stream)
     return C
+
+
+from .grouped import (  # noqa: E402  (uses the names above)
+    DG_RAGGED_K, DG_RAGGED_M, DgGroupedDesc, DgQweightDesc, dg_gemm_grouped,
+    dg_gemm_grouped_describe, dg_gemm_qweight, dg_gemm_qweight_describe, gemm_grouped,
+    gemm_grouped_k, gemm_qweight, make_grouped_desc, make_qweight_desc)

@@ -47,6 +47,8 @@ SOURCES = [
     "kernel_mfma_f32.hip",
     "tiles_f32.cpp",
     "kernel_sliver.hip",
+    "grouped_api.cpp",
+    "kernel_grouped_generic.hip",
 ]
 
 

@@ -17,6 +17,7 @@
 #include <mutex>
 
 #include "../../include/densegemm.h"
+#include "checks.hpp"
 #include "launch.hpp"
 
 using namespace dg;
@@ -37,48 +38,10 @@ constexpr int64_t kNumCu = 256;          // MI355X compute units
 constexpr int32_t kDefaultGroupM = 4;
 constexpr int32_t kMaxSplits = 256;
 
-int64_t elem_size(int32_t t) { return t == DG_F32 ? 4 : 2; }
-
-bool mul_ok(int64_t a, int64_t b, int64_t *out) { return !__builtin_mul_overflow(a, b, out); }
-bool add_ok(int64_t a, int64_t b, int64_t *out) { return !__builtin_add_overflow(a, b, out); }
-
-// Elements spanned by one rows x cols matrix with the given order and ld.
-bool matrix_span(int32_t order, int64_t rows, int64_t cols, int64_t ld, int64_t *span)
-{
-    if (rows == 0 || cols == 0) {
-        *span = 0;
-        return true;
-    }
-    int64_t outer = order == DG_ROW_MAJOR ? rows : cols;
-    int64_t inner = order == DG_ROW_MAJOR ? cols : rows;
-    int64_t t;
-    return mul_ok(outer - 1, ld, &t) && add_ok(t, inner, span);
-}
-
-// Elements spanned by the whole batch.
-bool batch_span(int64_t span, int64_t batch, int64_t stride, int64_t *total)
-{
-    if (span == 0 || batch == 0) {
-        *total = 0;
-        return true;
-    }
-    int64_t t;
-    return mul_ok(batch - 1, stride, &t) && add_ok(t, span, total);
-}
-
 struct Extents {
     int64_t a_bytes, b_bytes, c_bytes, bias_bytes;
     int64_t c_span;
 };
-
-bool ranges_overlap(const void *p, int64_t pn, const void *q, int64_t qn)
-{
-    if (!p || !q || pn <= 0 || qn <= 0)
-        return false;
-    uintptr_t a0 = (uintptr_t)p, a1 = a0 + (uintptr_t)pn;
-    uintptr_t b0 = (uintptr_t)q, b1 = b0 + (uintptr_t)qn;
-    return a0 < b1 && b0 < a1;
-}
 
 bool is_noop(const dg_gemm_desc *d) { return d->M == 0 || d->N == 0 || d->batch == 0; }
 
@@ -177,8 +140,6 @@ dg_status validate_ptrs(const dg_gemm_desc *d, const Extents &e, const void *A, 
     return DG_SUCCESS;
 }
 
-bool aligned_to(const void *p, int64_t bytes) { return ((uintptr_t)p % bytes) == 0; }
-
 // Batch strides keep every batch entry's A and B 16-byte aligned (they are
 // not used when batch == 1).
 bool strides_aligned(const dg_gemm_desc *d, int64_t elems)
@@ -213,8 +174,6 @@ bool k_contiguous(const dg_gemm_desc *d)
 {
     return d->a_order == DG_ROW_MAJOR && d->b_order == DG_COL_MAJOR;
 }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 int64_t tiles_of(const dg_gemm_desc *d, const TileConfig &t)
 {
@@ -329,7 +288,6 @@ TileConfig pick_quantised(const dg_gemm_desc *d, const TileConfig *table, int n)
         return t256;
     return t128;
 }
-
 
 // Split-K slices for `tiles` output tiles: only when the tiles alone leave
 // most compute units idle and every slice keeps a long K range: 1024 for
@@ -451,7 +409,6 @@ dg_status finish_plan(const dg_gemm_desc *d, Plan p, size_t ws_avail, bool ws_kn
     *plan = p;
     return DG_SUCCESS;
 }
-
 
 // `key`: the problem to look up in the tuned table (default d).  `keep`:
 // without a tuned or forced entry, plan on this tile of the family instead

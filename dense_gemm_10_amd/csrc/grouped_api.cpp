@@ -1,0 +1,373 @@
+// C ABI of the products over groups of rows and of the products with 4-bit
+// weights: host-side validation (no HIP calls), choice of the kernel and
+// launch.  Nothing is known of the groups' lengths here: the grid covers an
+// upper bound of the tiles, and the choice goes by the mean length.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+#include <stdio.h>
+#include <string.h>
+
+#include "../../include/densegemm.h"
+#include "checks.hpp"
+#include "grouped.hpp"
+
+using namespace dg;
+
+namespace {
+
+constexpr int64_t kMaxGroups = 65536;
+constexpr int64_t kMaxRows = INT32_MAX;
+
+bool dtype_ok(int32_t t) { return t == DG_F32 || t == DG_BF16 || t == DG_F16; }
+bool act_ok(int32_t a) { return a >= DG_ACT_NONE && a <= DG_ACT_GELU_TANH; }
+
+// Bytes of `count` matrices of `rows` rows of `len` elements, `ld` apart,
+// `stride` from one matrix to the next.
+bool bytes_of(int64_t count, int64_t stride, int64_t rows, int64_t len, int64_t ld, int64_t es,
+              int64_t *bytes)
+{
+    int64_t span, total;
+    return matrix_span(DG_ROW_MAJOR, rows, len, ld, &span) &&
+           batch_span(span, count, stride, &total) && mul_ok(total, es, bytes);
+}
+
+// Row tiles of a launch over groups of unknown lengths.
+int64_t row_tiles(int64_t rows, int64_t groups, int64_t bm)
+{
+    return rows / bm + (groups < rows ? groups : rows);
+}
+
+// A grid of `a` x `b` workgroups of 256 threads, if a launch can have it.
+bool grid_ok(int64_t a, int64_t b, uint32_t *programs)
+{
+    int64_t p;
+    if (!mul_ok(a, b, &p) || p > (int64_t)UINT32_MAX / 256)
+        return false;
+    *programs = (uint32_t)p;
+    return true;
+}
+
+// ---- grouped products -------------------------------------------------------
+
+struct Spans {
+    int64_t a, b, c, bias, offsets;      // bytes
+};
+
+bool reads_ab(const dg_grouped_desc *d)
+{
+    return d->alpha != 0.0f && d->rows > 0 && (d->ragged == DG_RAGGED_K || d->K > 0);
+}
+
+bool is_noop(const dg_grouped_desc *d)
+{
+    return d->groups == 0 || d->N == 0 ||
+           (d->ragged == DG_RAGGED_M ? d->rows == 0 : d->M == 0);
+}
+
+dg_status validate(const dg_grouped_desc *d, Spans *s)
+{
+    if (!d || d->struct_size != sizeof(dg_grouped_desc))
+        return DG_ERROR_INVALID_VALUE;
+    if (d->ragged != DG_RAGGED_M && d->ragged != DG_RAGGED_K)
+        return DG_ERROR_INVALID_VALUE;
+    const bool rk = d->ragged == DG_RAGGED_K;
+    if (!dtype_ok(d->a_type) || !dtype_ok(d->b_type) || !dtype_ok(d->c_type) ||
+        (d->b_order != DG_ROW_MAJOR && d->b_order != DG_COL_MAJOR) || !act_ok(d->act))
+        return DG_ERROR_INVALID_VALUE;
+    if (d->groups < 0 || d->rows < 0 || d->N < 0 || (rk ? d->M : d->K) < 0)
+        return DG_ERROR_INVALID_VALUE;
+    if (d->bias && !dtype_ok(d->bias_type))
+        return DG_ERROR_INVALID_VALUE;
+    const int64_t a_len = rk ? d->M : d->K;
+    const int64_t b_len = rk || d->b_order == DG_ROW_MAJOR ? d->N : d->K;
+    if (d->lda < 1 || d->ldb < 1 || d->ldc < 1 || d->lda < a_len || d->ldb < b_len ||
+        d->ldc < d->N)
+        return DG_ERROR_INVALID_VALUE;
+    if ((rk ? d->stride_c : d->stride_b) < 0 || (d->bias && d->stride_bias < 0))
+        return DG_ERROR_INVALID_VALUE;
+    if (d->a_type != d->b_type || (d->a_type == DG_F32 && d->c_type != DG_F32))
+        return DG_ERROR_NOT_SUPPORTED;
+    if (d->groups > kMaxGroups || d->rows > kMaxRows)
+        return DG_ERROR_NOT_SUPPORTED;
+    if (rk && (d->b_order != DG_ROW_MAJOR || d->bias || d->act != DG_ACT_NONE))
+        return DG_ERROR_NOT_SUPPORTED;
+    const int64_t es = elem_size(d->a_type), cs = elem_size(d->c_type);
+    s->offsets = (d->groups + 1) * 4;
+    s->bias = 0;
+    bool ok;
+    if (rk) {
+        ok = bytes_of(1, 0, d->rows, d->M, d->lda, es, &s->a) &&
+             bytes_of(1, 0, d->rows, d->N, d->ldb, es, &s->b) &&
+             bytes_of(d->groups, d->stride_c, d->M, d->N, d->ldc, cs, &s->c);
+        int64_t one;
+        if (ok && d->groups > 1 && d->M > 0 && d->N > 0 &&
+            (!matrix_span(DG_ROW_MAJOR, d->M, d->N, d->ldc, &one) || d->stride_c < one))
+            return DG_ERROR_INVALID_VALUE;       // C matrices overlap
+    } else {
+        const bool row = d->b_order == DG_ROW_MAJOR;
+        ok = bytes_of(1, 0, d->rows, d->K, d->lda, es, &s->a) &&
+             bytes_of(d->groups, d->stride_b, row ? d->K : d->N, row ? d->N : d->K, d->ldb, es,
+                      &s->b) &&
+             bytes_of(1, 0, d->rows, d->N, d->ldc, cs, &s->c);
+        if (d->bias)
+            ok = ok && bytes_of(d->groups, d->stride_bias, 1, d->N, d->N > 0 ? d->N : 1,
+                                elem_size(d->bias_type), &s->bias);
+    }
+    return ok ? DG_SUCCESS : DG_ERROR_INVALID_VALUE;
+}
+
+enum GroupedKernel { GROUPED_GENERIC };
+
+struct GroupedPlan {
+    GroupedKernel kernel;
+    const char *name;
+    int32_t bm, bn;
+    uint32_t programs;
+};
+
+dg_status plan_tiles(const dg_grouped_desc *d, GroupedPlan *p)
+{
+    const int64_t tn = ceil_div(d->N, p->bn);
+    const int64_t tm = d->ragged == DG_RAGGED_K ? ceil_div(d->M, p->bm)
+                                                : row_tiles(d->rows, d->groups, p->bm);
+    int64_t t;
+    if (!mul_ok(tm, tn, &t) || t > INT32_MAX ||
+        !grid_ok(t, d->ragged == DG_RAGGED_K ? d->groups : 1, &p->programs))
+        return DG_ERROR_NOT_SUPPORTED;
+    return DG_SUCCESS;
+}
+
+dg_status make_plan(const dg_grouped_desc *d, const void *A, const void *B, GroupedPlan *p)
+{
+    p->kernel = GROUPED_GENERIC;
+    p->name = "generic";
+    p->bm = p->bn = kGroupedGenericTile;
+    return plan_tiles(d, p);
+}
+
+// ---- 4-bit weights ----------------------------------------------------------
+
+struct QSpans {
+    int64_t a, q, scales, zeros, c, bias, offsets;
+};
+
+bool is_noop(const dg_qweight_desc *d) { return d->groups == 0 || d->N == 0 || d->M == 0; }
+bool reads_ab(const dg_qweight_desc *d) { return d->alpha != 0.0f && d->K > 0; }
+
+dg_status validate(const dg_qweight_desc *d, QSpans *s)
+{
+    if (!d || d->struct_size != sizeof(dg_qweight_desc))
+        return DG_ERROR_INVALID_VALUE;
+    if (!dtype_ok(d->a_type) || !dtype_ok(d->c_type) || !dtype_ok(d->scale_type) ||
+        (d->bias && !dtype_ok(d->bias_type)) || !act_ok(d->act))
+        return DG_ERROR_INVALID_VALUE;
+    if (d->groups < 0 || d->M < 0 || d->N < 0 || d->K < 0 || d->group_size < 1)
+        return DG_ERROR_INVALID_VALUE;
+    const int64_t qlen = d->K / 2 + d->K % 2;
+    const int64_t slen = d->K / d->group_size + (d->K % d->group_size != 0);
+    if (d->lda < 1 || d->ldc < 1 || d->ldq < 1 || d->lds < 1 || d->lda < d->K || d->ldc < d->N ||
+        d->ldq < qlen || d->lds < slen)
+        return DG_ERROR_INVALID_VALUE;
+    if (d->stride_q < 0 || d->stride_s < 0 || (d->bias && d->stride_bias < 0))
+        return DG_ERROR_INVALID_VALUE;
+    if (d->a_type == DG_F32 || d->group_size % 32 != 0)
+        return DG_ERROR_NOT_SUPPORTED;
+    if (d->groups > kMaxGroups || d->M > kMaxRows)
+        return DG_ERROR_NOT_SUPPORTED;
+    s->offsets = (d->groups + 1) * 4;
+    s->bias = 0;
+    const bool ok =
+        bytes_of(1, 0, d->M, d->K, d->lda, 2, &s->a) &&
+        bytes_of(d->groups, d->stride_q, d->N, qlen, d->ldq, 1, &s->q) &&
+        bytes_of(d->groups, d->stride_s, d->N, slen, d->lds, elem_size(d->scale_type),
+                 &s->scales) &&
+        bytes_of(d->groups, d->stride_s, d->N, slen, d->lds, 1, &s->zeros) &&
+        bytes_of(1, 0, d->M, d->N, d->ldc, elem_size(d->c_type), &s->c) &&
+        (!d->bias || bytes_of(d->groups, d->stride_bias, 1, d->N, d->N > 0 ? d->N : 1,
+                              elem_size(d->bias_type), &s->bias));
+    return ok ? DG_SUCCESS : DG_ERROR_INVALID_VALUE;
+}
+
+enum QweightKernel { QWEIGHT_GENERIC };
+
+struct QweightPlan {
+    QweightKernel kernel;
+    const char *name;
+    int32_t bm, bn;
+    uint32_t programs;
+};
+
+dg_status plan_tiles(const dg_qweight_desc *d, bool offsets, QweightPlan *p)
+{
+    const int64_t tn = ceil_div(d->N, p->bn);
+    const int64_t tm = offsets ? row_tiles(d->M, d->groups, p->bm) : ceil_div(d->M, p->bm);
+    return grid_ok(tm, tn, &p->programs) ? DG_SUCCESS : DG_ERROR_NOT_SUPPORTED;
+}
+
+dg_status make_plan(const dg_qweight_desc *d, bool offsets, const void *A, const void *Q,
+                    QweightPlan *p)
+{
+    p->kernel = QWEIGHT_GENERIC;
+    p->name = "generic";
+    p->bm = p->bn = kGroupedGenericTile;
+    return plan_tiles(d, offsets, p);
+}
+
+} // namespace
+
+extern "C" {
+
+dg_status dg_gemm_grouped(const dg_grouped_desc *d, const void *A, const void *B, void *C,
+                          const int32_t *offsets, void *stream)
+{
+    Spans sp;
+    dg_status st = validate(d, &sp);
+    if (st != DG_SUCCESS)
+        return st;
+    if (is_noop(d))
+        return DG_SUCCESS;
+    if (!C || !offsets || (reads_ab(d) && (!A || !B)))
+        return DG_ERROR_INVALID_VALUE;
+    if (!aligned_to(A, elem_size(d->a_type)) || !aligned_to(B, elem_size(d->b_type)) ||
+        !aligned_to(C, elem_size(d->c_type)) || !aligned_to(offsets, 4) ||
+        (d->bias && !aligned_to(d->bias, elem_size(d->bias_type))))
+        return DG_ERROR_INVALID_VALUE;
+    if ((reads_ab(d) && (ranges_overlap(C, sp.c, A, sp.a) || ranges_overlap(C, sp.c, B, sp.b))) ||
+        ranges_overlap(C, sp.c, d->bias, sp.bias) || ranges_overlap(C, sp.c, offsets, sp.offsets))
+        return DG_ERROR_INVALID_VALUE;
+    GroupedPlan p;
+    st = make_plan(d, A, B, &p);
+    if (st != DG_SUCCESS)
+        return st;
+    const bool rk = d->ragged == DG_RAGGED_K;
+    GroupedArgs a;
+    memset(&a, 0, sizeof a);
+    a.g.A = A;
+    a.g.B = B;
+    a.g.C = C;
+    a.g.bias = d->bias;
+    a.g.M = rk ? d->M : 0;
+    a.g.N = d->N;
+    a.g.K = rk ? 0 : d->K;
+    a.g.lda = d->lda;
+    a.g.ldb = d->ldb;
+    a.g.ldc = d->ldc;
+    a.g.sb = rk ? 0 : d->stride_b;
+    a.g.sc = rk ? d->stride_c : 0;
+    a.g.alpha = d->alpha;
+    a.g.beta = d->beta;
+    a.g.a_col = rk;
+    a.g.b_col = d->b_order == DG_COL_MAJOR;
+    a.g.c_type = d->c_type;
+    a.g.bias_type = d->bias_type;
+    a.g.act = d->act;
+    a.g.ab_type = d->a_type;
+    a.offsets = offsets;
+    a.groups = (int32_t)d->groups;
+    a.rows = (int32_t)d->rows;
+    a.stride_bias = d->stride_bias;
+    a.tiles_n = (uint32_t)ceil_div(d->N, p.bn);
+    a.tiles = rk ? (uint32_t)(ceil_div(d->M, p.bm) * a.tiles_n) : 0;
+    const hipError_t err = launch_grouped_generic(a, rk, p.programs, (hipStream_t)stream);
+    return err == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
+}
+
+dg_status dg_gemm_grouped_describe(const dg_grouped_desc *d, char *buf, size_t len)
+{
+    if (!buf || len == 0)
+        return DG_ERROR_INVALID_VALUE;
+    Spans sp;
+    dg_status st = validate(d, &sp);
+    if (st != DG_SUCCESS)
+        return st;
+    if (is_noop(d)) {
+        snprintf(buf, len, "noop");
+        return DG_SUCCESS;
+    }
+    GroupedPlan p;
+    st = make_plan(d, nullptr, nullptr, &p);
+    if (st == DG_SUCCESS)
+        snprintf(buf, len, "kernel=%s bm=%d bn=%d programs=%u", p.name, p.bm, p.bn, p.programs);
+    return st;
+}
+
+dg_status dg_gemm_qweight(const dg_qweight_desc *d, const void *A, const void *Q,
+                          const void *scales, const void *zeros, void *C, const int32_t *offsets,
+                          void *stream)
+{
+    QSpans sp;
+    dg_status st = validate(d, &sp);
+    if (st != DG_SUCCESS)
+        return st;
+    if (!offsets && d->groups > 1)
+        return DG_ERROR_INVALID_VALUE;
+    if (is_noop(d))
+        return DG_SUCCESS;
+    if (!C || (reads_ab(d) && (!A || !Q || !scales)))
+        return DG_ERROR_INVALID_VALUE;
+    if (!aligned_to(A, 2) || !aligned_to(scales, elem_size(d->scale_type)) ||
+        !aligned_to(C, elem_size(d->c_type)) || !aligned_to(offsets, 4) ||
+        (d->bias && !aligned_to(d->bias, elem_size(d->bias_type))))
+        return DG_ERROR_INVALID_VALUE;
+    if ((reads_ab(d) &&
+         (ranges_overlap(C, sp.c, A, sp.a) || ranges_overlap(C, sp.c, Q, sp.q) ||
+          ranges_overlap(C, sp.c, scales, sp.scales) || ranges_overlap(C, sp.c, zeros, sp.zeros))) ||
+        ranges_overlap(C, sp.c, d->bias, sp.bias) || ranges_overlap(C, sp.c, offsets, sp.offsets))
+        return DG_ERROR_INVALID_VALUE;
+    QweightPlan p;
+    st = make_plan(d, offsets != nullptr, A, Q, &p);
+    if (st != DG_SUCCESS)
+        return st;
+    QweightArgs a;
+    memset(&a, 0, sizeof a);
+    a.A = A;
+    a.Q = (const uint8_t *)Q;
+    a.scales = scales;
+    a.zeros = (const uint8_t *)zeros;
+    a.C = C;
+    a.bias = d->bias;
+    a.offsets = offsets;
+    a.groups = (int32_t)d->groups;
+    a.rows = (int32_t)d->M;
+    a.N = d->N;
+    a.K = d->K;
+    a.group_size = d->group_size;
+    a.lda = d->lda;
+    a.ldc = d->ldc;
+    a.ldq = d->ldq;
+    a.lds = d->lds;
+    a.stride_q = d->stride_q;
+    a.stride_s = d->stride_s;
+    a.stride_bias = d->stride_bias;
+    a.alpha = d->alpha;
+    a.beta = d->beta;
+    a.a_type = d->a_type;
+    a.c_type = d->c_type;
+    a.scale_type = d->scale_type;
+    a.bias_type = d->bias_type;
+    a.act = d->act;
+    a.tiles_n = (uint32_t)ceil_div(d->N, p.bn);
+    const hipError_t err = launch_qweight_generic(a, p.programs, (hipStream_t)stream);
+    return err == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
+}
+
+dg_status dg_gemm_qweight_describe(const dg_qweight_desc *d, char *buf, size_t len)
+{
+    if (!buf || len == 0)
+        return DG_ERROR_INVALID_VALUE;
+    QSpans sp;
+    dg_status st = validate(d, &sp);
+    if (st != DG_SUCCESS)
+        return st;
+    if (is_noop(d)) {
+        snprintf(buf, len, "noop");
+        return DG_SUCCESS;
+    }
+    QweightPlan p;
+    st = make_plan(d, d->groups > 1, nullptr, nullptr, &p);
+    if (st == DG_SUCCESS)
+        snprintf(buf, len, "kernel=%s bm=%d bn=%d programs=%u", p.name, p.bm, p.bn, p.programs);
+    return st;
+}
+
+} // extern "C"

@@ -266,6 +266,134 @@ dg_status dg_schedule_map(int64_t M, int64_t N, int64_t batch, int32_t split_k, 
                           int32_t bn, int32_t group_m, int32_t xcd_remap, int32_t *out,
                           int64_t out_len);
 
+/* ---- products over groups of rows ------------------------------------------
+ *
+ * A layer of experts multiplies the rows routed to each expert by that
+ * expert's matrix.  The rows of one group are consecutive, the groups have
+ * any lengths, and the lengths are known on the GPU only:
+ *
+ *   offsets  a DEVICE array of groups + 1 int32; group e is rows
+ *            [offsets[e], offsets[e+1]).  Values are clamped to [0, rows]
+ *            and made non-decreasing by a running maximum before use, so no
+ *            content of the array makes a call read or write outside its
+ *            operands; a group may be empty.  Rows before offsets[0] and
+ *            from offsets[groups] on belong to no group.
+ *
+ * DG_RAGGED_M (a layer's forward pass, and with B transposed its input
+ * gradient): for each row i of group e
+ *
+ *     C[i,:] = act( alpha * A[i,:] . B[e] + beta * C[i,:] + bias[e] )
+ *
+ *   A rows x K row-major, B[e] K x N in either order, C rows x N row-major.
+ *   Rows of C that belong to no group are neither read nor written, and the
+ *   same rows of A are not used.
+ *
+ * DG_RAGGED_K (the weight gradient): for each group e
+ *
+ *     C[e] = alpha * A[rows of e]^T . B[rows of e] + beta * C[e]
+ *
+ *   A rows x M row-major, B rows x N row-major, C[e] M x N row-major.  An
+ *   empty group gives beta * C[e] (0 when beta == 0).  No bias, no
+ *   activation; the bias gradient is the same call with M = 1 and an A of
+ *   ones.
+ *
+ * Types, accumulation, rounding, ownership, streams and errors as in
+ * dg_gemm; no workspace, nothing allocated, nothing read back, so calls may
+ * be captured into HIP graphs (a replay reads the offsets anew).  The work
+ * is planned from rows and groups; the offsets decide only which part of it
+ * each workgroup does. */
+typedef enum { DG_RAGGED_M = 0, DG_RAGGED_K = 1 } dg_ragged;
+
+/*
+ * All integer fields are in ELEMENTS.
+ *   struct_size     sizeof(dg_grouped_desc).
+ *   ragged          dg_ragged.
+ *   a_type ...      as in dg_gemm_desc: (F32, F32, F32) or (X, X, c) with X
+ *                   = BF16 or F16 and c any type.
+ *   b_order         order of each B[e]; RAGGED_K: DG_ROW_MAJOR.
+ *   groups          0 .. 65536; 0 is a no-op.
+ *   rows            0 .. 2^31 - 1, the allocated rows of A (and C or B).
+ *   M               RAGGED_K only.    K  RAGGED_M only.    (else ignored)
+ *   lda, ldb, ldc   leading dimensions, each >= max(1, the row's length).
+ *   stride_b        RAGGED_M: distance of consecutive B[e] (0: one B).
+ *   stride_c        RAGGED_K: distance of consecutive C[e], which must not
+ *                   overlap.
+ *   bias            RAGGED_M: optional DEVICE array; bias[e] is N elements
+ *                   at e * stride_bias (0: one bias).
+ *   alpha, beta, act as in dg_gemm_desc.
+ */
+typedef struct dg_grouped_desc {
+    uint32_t struct_size;
+    int32_t ragged;
+    int32_t a_type, b_type, c_type, bias_type;
+    int32_t b_order;
+    int32_t act;
+    int64_t groups, rows;
+    int64_t M, N, K;
+    int64_t lda, ldb, ldc;
+    int64_t stride_b, stride_c, stride_bias;
+    float alpha, beta;
+    const void *bias;
+} dg_grouped_desc;
+
+/* Enqueue the products on `stream`. */
+dg_status dg_gemm_grouped(const dg_grouped_desc *d, const void *A, const void *B, void *C,
+                          const int32_t *offsets, void *stream);
+
+/* One line on the kernel, tile and grid dg_gemm_grouped would run (operands
+ * taken as aligned). */
+dg_status dg_gemm_grouped_describe(const dg_grouped_desc *d, char *buf, size_t len);
+
+/* ---- products with 4-bit weights --------------------------------------------
+ *
+ *     C = act( alpha * A . W^T + beta * C + bias )
+ *     W[n][k] = scale[n][k / group_size] * (q[n][k] - zero[n][k / group_size])
+ *
+ * with A M x K row-major in BF16 or F16, C M x N row-major, q in 0 .. 15.
+ *   Q       row n at byte n * ldq, ceil(K / 2) bytes: q[n][2j] is the low
+ *           and q[n][2j+1] the high half of byte j.
+ *   scales  scale[n][j] at element n * lds + j, ceil(K / group_size) of them.
+ *   zeros   one byte each, laid out as the scales (values 0 .. 15; the low
+ *           four bits count); NULL: every zero is 8.
+ * With offsets, row i of A and C uses the weights of the group that holds
+ * it, W[e] at Q + e * stride_q bytes, scales and zeros + e * stride_s, bias
+ * + e * stride_bias; the offsets as above, with M in the place of rows, and
+ * rows of no group left as they were.  offsets may be NULL when groups == 1:
+ * all M rows then use the one W.
+ * W is never rounded to 16 bits: the scales and zeros enter in fp32.
+ *
+ *   struct_size  sizeof(dg_qweight_desc).
+ *   a_type       BF16 or F16 (F32: DG_ERROR_NOT_SUPPORTED).
+ *   c_type, scale_type, bias_type   any dg_dtype.
+ *   groups       1 .. 65536 weight matrices (0 is a no-op).
+ *   M            0 .. 2^31 - 1 rows.
+ *   group_size   a positive multiple of 32 (else DG_ERROR_NOT_SUPPORTED);
+ *                the last group of a row may be shorter.
+ *   lda, ldc, lds in elements (lds also for zeros), ldq and stride_q in
+ *                bytes; lda >= max(1, K), ldc >= max(1, N), ldq >=
+ *                max(1, ceil(K / 2)), lds >= max(1, ceil(K / group_size)).
+ */
+typedef struct dg_qweight_desc {
+    uint32_t struct_size;
+    int32_t a_type, c_type, scale_type, bias_type;
+    int32_t act;
+    int64_t groups;
+    int64_t M, N, K, group_size;
+    int64_t lda, ldc, ldq, lds;
+    int64_t stride_q, stride_s, stride_bias;
+    float alpha, beta;
+    const void *bias;
+} dg_qweight_desc;
+
+/* Enqueue the product on `stream`.  Needs no workspace; may be captured. */
+dg_status dg_gemm_qweight(const dg_qweight_desc *d, const void *A, const void *Q,
+                          const void *scales, const void *zeros, void *C,
+                          const int32_t *offsets, void *stream);
+
+/* One line on the kernel, tile and grid dg_gemm_qweight would run (operands
+ * taken as aligned). */
+dg_status dg_gemm_qweight_describe(const dg_qweight_desc *d, char *buf, size_t len);
+
 #ifdef __cplusplus
 }
 #endif
