@@ -49,6 +49,10 @@ SOURCES = [
     "kernel_sliver.hip",
     "grouped_api.cpp",
     "kernel_grouped_generic.hip",
+    "kernel_grouped16_m256.hip",
+    "kernel_grouped16_m128.hip",
+    "kernel_grouped16_k256.hip",
+    "kernel_grouped16_k128.hip",
 ]
 
 

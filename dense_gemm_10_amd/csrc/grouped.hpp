@@ -204,6 +204,11 @@ struct QweightArgs {
 // Launchers; each returns hipSuccess or the launch error.
 hipError_t launch_grouped_generic(const GroupedArgs &a, bool ragged_k, uint32_t programs,
                                   hipStream_t s);
+// 16-bit matrix-core tiles (256 x 256 and 128 x 128)
+hipError_t launch_grouped16_m256(const GroupedArgs &a, uint32_t programs, hipStream_t s);
+hipError_t launch_grouped16_m128(const GroupedArgs &a, uint32_t programs, hipStream_t s);
+hipError_t launch_grouped16_k256(const GroupedArgs &a, uint32_t programs, hipStream_t s);
+hipError_t launch_grouped16_k128(const GroupedArgs &a, uint32_t programs, hipStream_t s);
 hipError_t launch_qweight_generic(const QweightArgs &a, uint32_t programs, hipStream_t s);
 
 constexpr int kGroupedGenericTile = 64;

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 #include <stdio.h>
+#include <stdlib.h>
 #include <string.h>
 
 #include "../../include/densegemm.h"
@@ -116,33 +117,68 @@ dg_status validate(const dg_grouped_desc *d, Spans *s)
     return ok ? DG_SUCCESS : DG_ERROR_INVALID_VALUE;
 }
 
-enum GroupedKernel { GROUPED_GENERIC };
+using GroupedLaunch = hipError_t (*)(const GroupedArgs &, uint32_t, hipStream_t);
 
-struct GroupedPlan {
-    GroupedKernel kernel;
+// A kernel of the grouped products: its tile and its launchers.
+struct GroupedKernel {
     const char *name;
     int32_t bm, bn;
+    GroupedLaunch ragged_m, ragged_k;
+};
+
+hipError_t generic_m(const GroupedArgs &a, uint32_t p, hipStream_t s)
+{
+    return launch_grouped_generic(a, false, p, s);
+}
+hipError_t generic_k(const GroupedArgs &a, uint32_t p, hipStream_t s)
+{
+    return launch_grouped_generic(a, true, p, s);
+}
+
+const GroupedKernel kGeneric = {"generic", kGroupedGenericTile, kGroupedGenericTile, generic_m,
+                                generic_k};
+const GroupedKernel kTile256 = {"mfma16_256x256", 256, 256, launch_grouped16_m256,
+                                launch_grouped16_k256};
+const GroupedKernel kTile128 = {"mfma16_128x128", 128, 128, launch_grouped16_m128,
+                                launch_grouped16_k128};
+
+struct GroupedPlan {
+    const GroupedKernel *kernel;
     uint32_t programs;
 };
 
-dg_status plan_tiles(const dg_grouped_desc *d, GroupedPlan *p)
+// The 16-bit matrix-core tiles read whole 16-byte pieces of rows and
+// address a tile with 32-bit byte offsets.
+bool mfma16_ok(const dg_grouped_desc *d, const void *A, const void *B)
 {
-    const int64_t tn = ceil_div(d->N, p->bn);
-    const int64_t tm = d->ragged == DG_RAGGED_K ? ceil_div(d->M, p->bm)
-                                                : row_tiles(d->rows, d->groups, p->bm);
+    return d->a_type != DG_F32 && aligned_to(A, 16) && aligned_to(B, 16) && d->lda % 8 == 0 &&
+           d->ldb % 8 == 0 && d->lda < (1 << 22) && d->ldb < (1 << 22) &&
+           (d->ragged == DG_RAGGED_K || d->groups <= 1 || d->stride_b % 8 == 0);
+}
+
+const GroupedKernel *choose(const dg_grouped_desc *d, const void *A, const void *B)
+{
+    if (!mfma16_ok(d, A, B))
+        return &kGeneric;
+    if (const char *want = getenv("DG_FORCE_GROUPED"))
+        for (const GroupedKernel *k : {&kTile256, &kTile128})
+            if (!strcmp(want, k->name))
+                return k;
+    return &kTile256;
+}
+
+dg_status make_plan(const dg_grouped_desc *d, const void *A, const void *B, GroupedPlan *p)
+{
+    p->kernel = choose(d, A, B);
+    const int64_t bm = p->kernel->bm, bn = p->kernel->bn;
+    const int64_t tn = ceil_div(d->N, bn);
+    const int64_t tm = d->ragged == DG_RAGGED_K ? ceil_div(d->M, bm)
+                                                : row_tiles(d->rows, d->groups, bm);
     int64_t t;
     if (!mul_ok(tm, tn, &t) || t > INT32_MAX ||
         !grid_ok(t, d->ragged == DG_RAGGED_K ? d->groups : 1, &p->programs))
         return DG_ERROR_NOT_SUPPORTED;
     return DG_SUCCESS;
-}
-
-dg_status make_plan(const dg_grouped_desc *d, const void *A, const void *B, GroupedPlan *p)
-{
-    p->kernel = GROUPED_GENERIC;
-    p->name = "generic";
-    p->bm = p->bn = kGroupedGenericTile;
-    return plan_tiles(d, p);
 }
 
 // ---- 4-bit weights ----------------------------------------------------------
@@ -266,9 +302,10 @@ dg_status dg_gemm_grouped(const dg_grouped_desc *d, const void *A, const void *B
     a.groups = (int32_t)d->groups;
     a.rows = (int32_t)d->rows;
     a.stride_bias = d->stride_bias;
-    a.tiles_n = (uint32_t)ceil_div(d->N, p.bn);
-    a.tiles = rk ? (uint32_t)(ceil_div(d->M, p.bm) * a.tiles_n) : 0;
-    const hipError_t err = launch_grouped_generic(a, rk, p.programs, (hipStream_t)stream);
+    a.tiles_n = (uint32_t)ceil_div(d->N, p.kernel->bn);
+    a.tiles = rk ? (uint32_t)(ceil_div(d->M, p.kernel->bm) * a.tiles_n) : 0;
+    const hipError_t err =
+        (rk ? p.kernel->ragged_k : p.kernel->ragged_m)(a, p.programs, (hipStream_t)stream);
     return err == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
 }
 
@@ -287,7 +324,8 @@ dg_status dg_gemm_grouped_describe(const dg_grouped_desc *d, char *buf, size_t l
     GroupedPlan p;
     st = make_plan(d, nullptr, nullptr, &p);
     if (st == DG_SUCCESS)
-        snprintf(buf, len, "kernel=%s bm=%d bn=%d programs=%u", p.name, p.bm, p.bn, p.programs);
+        snprintf(buf, len, "kernel=%s bm=%d bn=%d programs=%u", p.kernel->name, p.kernel->bm,
+                 p.kernel->bn, p.programs);
     return st;
 }
 

@@ -1,0 +1,13 @@
+// Instantiations of the grouped 16-bit products (grouped16.hpp): ragged K,
+// 256 x 256 tile.
+#include "grouped16.hpp"
+
+namespace dg {
+
+hipError_t launch_grouped16_k256(const GroupedArgs &a, uint32_t programs, hipStream_t s)
+{
+    return a.g.ab_type == DT_F16 ? launch_grouped_k<DT_F16, 256, 256, 2, 64, 16>(a, programs, s)
+                                 : launch_grouped_k<DT_BF16, 256, 256, 2, 64, 16>(a, programs, s);
+}
+
+} // namespace dg
