@@ -53,6 +53,8 @@ SOURCES = [
     "kernel_grouped16_m128.hip",
     "kernel_grouped16_k256.hip",
     "kernel_grouped16_k128.hip",
+    "kernel_stream16.hip",
+    "kernel_qstream.hip",
 ]
 
 

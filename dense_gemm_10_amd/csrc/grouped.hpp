@@ -209,6 +209,11 @@ hipError_t launch_grouped16_m256(const GroupedArgs &a, uint32_t programs, hipStr
 hipError_t launch_grouped16_m128(const GroupedArgs &a, uint32_t programs, hipStream_t s);
 hipError_t launch_grouped16_k256(const GroupedArgs &a, uint32_t programs, hipStream_t s);
 hipError_t launch_grouped16_k128(const GroupedArgs &a, uint32_t programs, hipStream_t s);
+// few rows per group (kernel_stream16.hip)
+hipError_t launch_grouped_stream(int32_t variant, const GroupedArgs &a, uint32_t programs,
+                                 hipStream_t s);
+hipError_t launch_qweight_stream(int32_t variant, const QweightArgs &a, uint32_t programs,
+                                 hipStream_t s);
 hipError_t launch_qweight_generic(const QweightArgs &a, uint32_t programs, hipStream_t s);
 
 constexpr int kGroupedGenericTile = 64;

@@ -3,6 +3,7 @@
 // launch.  Nothing is known of the groups' lengths here: the grid covers an
 // upper bound of the tiles, and the choice goes by the mean length.
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <stdio.h>
 #include <stdlib.h>
@@ -18,6 +19,7 @@ namespace {
 
 constexpr int64_t kMaxGroups = 65536;
 constexpr int64_t kMaxRows = INT32_MAX;
+constexpr int kCus = 256;                // MI355X compute units
 
 bool dtype_ok(int32_t t) { return t == DG_F32 || t == DG_BF16 || t == DG_F16; }
 bool act_ok(int32_t a) { return a >= DG_ACT_NONE && a <= DG_ACT_GELU_TANH; }
@@ -38,11 +40,12 @@ int64_t row_tiles(int64_t rows, int64_t groups, int64_t bm)
     return rows / bm + (groups < rows ? groups : rows);
 }
 
-// A grid of `a` x `b` workgroups of 256 threads, if a launch can have it.
+// A grid of `a` x `b` workgroups of at most 1024 threads, if a launch can
+// have it.
 bool grid_ok(int64_t a, int64_t b, uint32_t *programs)
 {
     int64_t p;
-    if (!mul_ok(a, b, &p) || p > (int64_t)UINT32_MAX / 256)
+    if (!mul_ok(a, b, &p) || p > (int64_t)UINT32_MAX / 1024)
         return false;
     *programs = (uint32_t)p;
     return true;
@@ -119,7 +122,8 @@ dg_status validate(const dg_grouped_desc *d, Spans *s)
 
 using GroupedLaunch = hipError_t (*)(const GroupedArgs &, uint32_t, hipStream_t);
 
-// A kernel of the grouped products: its tile and its launchers.
+// A kernel of the grouped products: its tile and its launchers (null: not
+// for this kind).
 struct GroupedKernel {
     const char *name;
     int32_t bm, bn;
@@ -134,6 +138,11 @@ hipError_t generic_k(const GroupedArgs &a, uint32_t p, hipStream_t s)
 {
     return launch_grouped_generic(a, true, p, s);
 }
+template <int V>
+hipError_t stream_m(const GroupedArgs &a, uint32_t p, hipStream_t s)
+{
+    return launch_grouped_stream(V, a, p, s);
+}
 
 const GroupedKernel kGeneric = {"generic", kGroupedGenericTile, kGroupedGenericTile, generic_m,
                                 generic_k};
@@ -141,6 +150,23 @@ const GroupedKernel kTile256 = {"mfma16_256x256", 256, 256, launch_grouped16_m25
                                 launch_grouped16_k256};
 const GroupedKernel kTile128 = {"mfma16_128x128", 128, 128, launch_grouped16_m128,
                                 launch_grouped16_k128};
+const GroupedKernel kStream16x32 = {"stream16_16x32", 16, 32, stream_m<0>, nullptr};
+const GroupedKernel kStream16x64 = {"stream16_16x64", 16, 64, stream_m<1>, nullptr};
+const GroupedKernel kStream32x64 = {"stream16_32x64", 32, 64, stream_m<2>, nullptr};
+const GroupedKernel *const kGrouped16[] = {&kTile256, &kTile128, &kStream16x32, &kStream16x64,
+                                           &kStream32x64};
+
+// The kernel of `table` that DG_FORCE_GROUPED names (benchmarking and
+// tests), or NULL.
+template <typename K, size_t N>
+const K *forced_kernel(const K *const (&table)[N])
+{
+    const char *want = getenv("DG_FORCE_GROUPED");
+    for (const K *k : table)
+        if (want && !strcmp(want, k->name))
+            return k;
+    return nullptr;
+}
 
 struct GroupedPlan {
     const GroupedKernel *kernel;
@@ -156,15 +182,50 @@ bool mfma16_ok(const dg_grouped_desc *d, const void *A, const void *B)
            (d->ragged == DG_RAGGED_K || d->groups <= 1 || d->stride_b % 8 == 0);
 }
 
+// The kernel for a problem.  Group lengths are unknown; the mean stands for
+// them, and every group is taken to end inside a tile (0.6 of one lost).
+//
+// Ragged rows, by the mean rows of a group (us, MI355X, bf16):
+//   up to 8 rows, the 16-row streaming kernels: 64 groups, 512 rows, 2048 x
+//     2048: 98-100 against 98-118 on the 128 x 128 tile; 64 rows, 2048 x
+//     1024: 36 against 42-52.  32 columns per workgroup where 64 would make
+//     fewer than 512 workgroups (8 groups, 8 rows, 1024 x 1024: 5.5 against
+//     6.1-7.3);
+//   up to 16, the 32-row one: 1024 rows on those 64 groups 105 against
+//     112-120 on 16 rows, 4 groups, 64 rows, 4096 x 4096 31-34 against 43
+//     and 40-51 on the tile;
+//   above, a tile: the whole waves of 256 workgroups that each would make,
+//     at 1 a wave for 256 x 256 (one workgroup per CU) and 0.72 for 512
+//     workgroups of 128 x 128, half a wave added for their last one (8192
+//     rows, 16 groups, 4096 x 4096: 326 against 390; 4096 rows, 32 groups,
+//     2048 x 2048: 113 against 81).
+// Ragged K: the 128 x 128 tile, whose second workgroup on a CU covers the
+// other's epilogue (16 groups of 2048 x 2048, 8192 rows: 103 against 107;
+// 32 of 512 x 1024: 18-21 against 24), unless the groups are long and 256 x
+// 256 tiles fill the chip (8 of 1024 x 2048: 47 against 50).
 const GroupedKernel *choose(const dg_grouped_desc *d, const void *A, const void *B)
 {
     if (!mfma16_ok(d, A, B))
         return &kGeneric;
-    if (const char *want = getenv("DG_FORCE_GROUPED"))
-        for (const GroupedKernel *k : {&kTile256, &kTile128})
-            if (!strcmp(want, k->name))
-                return k;
-    return &kTile256;
+    const bool rk = d->ragged == DG_RAGGED_K;
+    if (const GroupedKernel *k = forced_kernel(kGrouped16))
+        if (rk ? k->ragged_k : k->ragged_m)
+            return k;
+    const double mean = (double)d->rows / (double)d->groups;
+    const double n256 = (double)ceil_div(d->N, 256), n128 = (double)ceil_div(d->N, 128);
+    if (rk) {
+        const double tiles = (double)d->groups * (double)ceil_div(d->M, 256) * n256;
+        return mean >= 768 && tiles >= 240 ? &kTile256 : &kTile128;
+    }
+    if (mean <= 8)
+        return row_tiles(d->rows, d->groups, 16) * ceil_div(d->N, 64) < 512 ? &kStream16x32
+                                                                            : &kStream16x64;
+    if (mean <= 16)
+        return &kStream32x64;
+    const double lost = 0.6 * (double)d->groups;
+    const double waves256 = ceil(((double)d->rows / 256 + lost) * n256 / kCus);
+    const double waves128 = ((double)d->rows / 128 + lost) * n128 / (2 * kCus) + 0.5;
+    return waves256 < 0.72 * waves128 ? &kTile256 : &kTile128;
 }
 
 dg_status make_plan(const dg_grouped_desc *d, const void *A, const void *B, GroupedPlan *p)
@@ -224,29 +285,77 @@ dg_status validate(const dg_qweight_desc *d, QSpans *s)
     return ok ? DG_SUCCESS : DG_ERROR_INVALID_VALUE;
 }
 
-enum QweightKernel { QWEIGHT_GENERIC };
+using QweightLaunch = hipError_t (*)(const QweightArgs &, uint32_t, hipStream_t);
 
-struct QweightPlan {
-    QweightKernel kernel;
+struct QweightKernel {
     const char *name;
     int32_t bm, bn;
+    QweightLaunch launch;
+};
+
+template <int V>
+hipError_t qstream(const QweightArgs &a, uint32_t p, hipStream_t s)
+{
+    return launch_qweight_stream(V, a, p, s);
+}
+
+const QweightKernel kQGeneric = {"generic", kGroupedGenericTile, kGroupedGenericTile,
+                                 launch_qweight_generic};
+const QweightKernel kQ16x16 = {"qstream_16x16", 16, 16, qstream<0>};
+const QweightKernel kQ16x32 = {"qstream_16x32", 16, 32, qstream<1>};
+const QweightKernel kQ16x64 = {"qstream_16x64", 16, 64, qstream<2>};
+const QweightKernel kQ32x32 = {"qstream_32x32", 32, 32, qstream<3>};
+const QweightKernel kQ32x64 = {"qstream_32x64", 32, 64, qstream<4>};
+const QweightKernel *const kQweight[] = {&kQ32x64, &kQ32x32, &kQ16x64, &kQ16x32, &kQ16x16};
+
+struct QweightPlan {
+    const QweightKernel *kernel;
     uint32_t programs;
 };
 
-dg_status plan_tiles(const dg_qweight_desc *d, bool offsets, QweightPlan *p)
+// The matrix-core kernels read A and Q in whole 16-byte pieces and K in
+// whole steps of 32.
+bool qstream_ok(const dg_qweight_desc *d, bool offsets, const void *A, const void *Q)
 {
-    const int64_t tn = ceil_div(d->N, p->bn);
-    const int64_t tm = offsets ? row_tiles(d->M, d->groups, p->bm) : ceil_div(d->M, p->bm);
-    return grid_ok(tm, tn, &p->programs) ? DG_SUCCESS : DG_ERROR_NOT_SUPPORTED;
+    return aligned_to(A, 16) && aligned_to(Q, 16) && d->lda % 8 == 0 && d->ldq % 16 == 0 &&
+           (!offsets || d->stride_q % 16 == 0) && d->K % 32 == 0 && d->K < INT32_MAX - 65536 &&
+           d->lda < (1 << 24) && d->ldq < (1 << 24) && d->lds < (1 << 22);
+}
+
+int64_t row_tiles(const dg_qweight_desc *d, bool offsets, const QweightKernel &k)
+{
+    return offsets ? row_tiles(d->M, d->groups, k.bm) : ceil_div(d->M, k.bm);
+}
+
+// 32 rows where a group has more than 16, and the widest workgroup (each
+// reads A once) that still makes 512 of them for up to 4 rows, 256 for
+// more, where A's traffic counts (us, bf16, group size 128):
+//   1 row,   4096 x 4096: 5.4 on 16 columns, 6.9 on 32, 10.4 on 64;
+//            16384 x 4096: 12.5, 10.2, 11.8;  8192 x 8192: 10.5, 12.6, 19.1
+//   16 rows, 4096 x 4096: 7.2, 9.2, 11.8;  16384 x 4096: 18.6, 14.0, 13.3
+//   64 rows, 16384 x 4096: 31.8 on 16 x 64, 31.6 on 32 x 32, 26.9 on 32 x 64
+const QweightKernel *choose(const dg_qweight_desc *d, bool offsets, const void *A, const void *Q)
+{
+    if (!qstream_ok(d, offsets, A, Q))
+        return &kQGeneric;
+    if (const QweightKernel *k = forced_kernel(kQweight))
+        return k;
+    const int64_t rows = offsets ? d->M / d->groups : d->M;
+    const int64_t want = rows <= 4 ? 512 : 256;
+    for (const QweightKernel *k : kQweight)
+        if ((k->bm == 16 || rows > 16) &&
+            ceil_div(d->N, k->bn) >= ceil_div(want, row_tiles(d, offsets, *k)))
+            return k;
+    return &kQ16x16;
 }
 
 dg_status make_plan(const dg_qweight_desc *d, bool offsets, const void *A, const void *Q,
                     QweightPlan *p)
 {
-    p->kernel = QWEIGHT_GENERIC;
-    p->name = "generic";
-    p->bm = p->bn = kGroupedGenericTile;
-    return plan_tiles(d, offsets, p);
+    p->kernel = choose(d, offsets, A, Q);
+    return grid_ok(row_tiles(d, offsets, *p->kernel), ceil_div(d->N, p->kernel->bn), &p->programs)
+               ? DG_SUCCESS
+               : DG_ERROR_NOT_SUPPORTED;
 }
 
 } // namespace
@@ -384,8 +493,8 @@ dg_status dg_gemm_qweight(const dg_qweight_desc *d, const void *A, const void *Q
     a.scale_type = d->scale_type;
     a.bias_type = d->bias_type;
     a.act = d->act;
-    a.tiles_n = (uint32_t)ceil_div(d->N, p.bn);
-    const hipError_t err = launch_qweight_generic(a, p.programs, (hipStream_t)stream);
+    a.tiles_n = (uint32_t)ceil_div(d->N, p.kernel->bn);
+    const hipError_t err = p.kernel->launch(a, p.programs, (hipStream_t)stream);
     return err == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
 }
 
@@ -404,7 +513,8 @@ dg_status dg_gemm_qweight_describe(const dg_qweight_desc *d, char *buf, size_t l
     QweightPlan p;
     st = make_plan(d, d->groups > 1, nullptr, nullptr, &p);
     if (st == DG_SUCCESS)
-        snprintf(buf, len, "kernel=%s bm=%d bn=%d programs=%u", p.name, p.bm, p.bn, p.programs);
+        snprintf(buf, len, "kernel=%s bm=%d bn=%d programs=%u", p.kernel->name, p.kernel->bm,
+                 p.kernel->bn, p.programs);
     return st;
 }
 

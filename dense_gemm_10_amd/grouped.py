@@ -9,8 +9,8 @@ from __future__ import annotations
 
 import ctypes
 
-from . import (DG_ROW_MAJOR, DG_SUCCESS, DgError, _ACT, _DTYPE, _ORDER, _enum, _load,
-               _torch_dtype_name)
+from . import (DG_BF16, DG_COL_MAJOR, DG_F16, DG_F32, DG_ROW_MAJOR, DG_SUCCESS, DgError, _ACT,
+               _DTYPE, _ORDER, _enum, _load)
 
 DG_RAGGED_M, DG_RAGGED_K = 0, 1
 _RAGGED = {"m": DG_RAGGED_M, "k": DG_RAGGED_K}
@@ -128,22 +128,36 @@ def dg_gemm_qweight_describe(desc):
 
 
 # ---- torch convenience -----------------------------------------------------------
-def _row_ld(t, name):
-    """Leading dimension of a 2-D row-major tensor (the last two dimensions
-    of a 3-D one)."""
-    rows, cols = t.shape[-2:]
-    r, c = t.stride()[-2:]
+# A call on a few rows runs for a few microseconds on the GPU, so the checks
+# below read each tensor's shape, strides, type and device once.
+_types = None
+
+
+def _code(t):
+    """dg_dtype of a tensor."""
+    global _types
+    if _types is None:
+        import torch
+        _types = {torch.float32: DG_F32, torch.bfloat16: DG_BF16, torch.float16: DG_F16}
+    code = _types.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
+
+
+def _row_ld(rows, cols, r, c, name):
+    """Leading dimension of a row-major matrix with strides (r, c)."""
     if (c != 1 and cols > 1) or (r < cols and rows > 1):
-        raise ValueError(f"{name}: strides {t.stride()} are not row-major; pass a contiguous tensor")
-    return max(r, cols, 1) if rows > 1 else max(cols, 1)
+        raise ValueError(f"{name}: strides ({r}, {c}) are not row-major; pass a contiguous tensor")
+    return r if rows > 1 and r > 0 else cols or 1
 
 
-def _same_device(A, **others):
-    if not A.is_cuda:
+def _same_device(device, **others):
+    if device < 0:
         raise ValueError("tensors must be on a GPU")
     for name, t in others.items():
-        if t is not None and t.device != A.device:
-            raise ValueError(f"{name} is on {t.device}, A on {A.device}")
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{name} is on another device than A")
 
 
 def _check_offsets(offsets, groups):
@@ -159,7 +173,7 @@ def _output(C, shape, dtype, A, beta):
             raise ValueError("beta != 0 needs an input C")
         import torch
         return torch.empty(shape, dtype=dtype or A.dtype, device=A.device)
-    if tuple(C.shape) != shape:
+    if C.shape != shape:
         raise ValueError(f"C: shape {tuple(C.shape)}, {shape} is wanted")
     if dtype is not None and C.dtype != dtype:
         raise ValueError(f"C is {C.dtype}, out_dtype {dtype}")
@@ -167,24 +181,26 @@ def _output(C, shape, dtype, A, beta):
 
 
 def _bias(bias, groups, N, grouped):
-    """(address, dtype name, stride) of a bias of N values, or one per group."""
+    """(address, type, stride) of a bias of N values, or one per group."""
     if bias is None:
-        return None, "f32", 0
+        return None, DG_F32, 0
     if tuple(bias.shape) not in ((N,), (groups, N)) or (bias.dim() == 2 and not grouped):
         raise ValueError(f"bias: shape {tuple(bias.shape)} for {groups} groups of {N} columns")
     if N > 1 and bias.stride(-1) != 1:
         raise ValueError("bias: the last dimension must be contiguous")
-    return bias.data_ptr(), _torch_dtype_name(bias), bias.stride(0) if bias.dim() == 2 else 0
+    return bias.data_ptr(), _code(bias), bias.stride(0) if bias.dim() == 2 else 0
 
 
-def _on_stream(A, stream, call):
-    """call(stream) with A's device current, on its current stream by default."""
+def _launch(entry, name, device, stream, *args):
+    """entry(*args, stream) with `device` current, on its current stream by
+    default."""
     import torch
-    index = A.device.index
-    if torch.cuda.current_device() == index:
-        return call(torch.cuda.current_stream(index).cuda_stream if stream is None else stream)
-    with torch.cuda.device(index):
-        return call(torch.cuda.current_stream(index).cuda_stream if stream is None else stream)
+    if torch.cuda.current_device() != device:
+        with torch.cuda.device(device):
+            return _launch(entry, name, device, stream, *args)
+    st = entry(*args, torch.cuda.current_stream(device).cuda_stream if stream is None else stream)
+    if st != DG_SUCCESS:
+        raise DgError(st, name)
 
 
 def gemm_grouped(A, B, offsets, C=None, *, alpha=1.0, beta=0.0, bias=None, act="none",
@@ -197,28 +213,29 @@ def gemm_grouped(A, B, offsets, C=None, *, alpha=1.0, beta=0.0, bias=None, act="
     offsets: int32 (groups + 1,) on the GPU.  bias: (groups, N) or (N,).
     Returns C (rows, N); rows of no group keep what they held (in a C
     allocated here: nothing defined)."""
-    if A.dim() != 2 or B.dim() != 3 or A.shape[1] != B.shape[1]:
-        raise ValueError(f"A {tuple(A.shape)} and B {tuple(B.shape)}: (rows, K) and (groups, K, N) are wanted")
-    rows, K = A.shape
-    groups, _, N = B.shape
+    ashape, bshape = A.shape, B.shape
+    if len(ashape) != 2 or len(bshape) != 3 or ashape[1] != bshape[1]:
+        raise ValueError(f"A {tuple(ashape)} and B {tuple(bshape)}: (rows, K) and (groups, K, N) are wanted")
+    rows, K = ashape
+    groups, _, N = bshape
     _check_offsets(offsets, groups)
     C = _output(C, (rows, N), out_dtype, A, beta)
-    _same_device(A, B=B, C=C, offsets=offsets, bias=bias)
+    device = A.get_device()
+    _same_device(device, B=B, C=C, offsets=offsets, bias=bias)
     sb, sk, sn = B.stride()
     if (sn == 1 or N <= 1) and (sk >= N or K <= 1):
-        order, ldb = "row", max(sk, N, 1) if K > 1 else max(N, 1)
+        order, ldb = DG_ROW_MAJOR, max(sk, N, 1) if K > 1 else max(N, 1)
     elif (sk == 1 or K <= 1) and (sn >= K or N <= 1):
-        order, ldb = "col", max(sn, K, 1) if N > 1 else max(K, 1)
+        order, ldb = DG_COL_MAJOR, max(sn, K, 1) if N > 1 else max(K, 1)
     else:
         raise ValueError(f"B: strides {B.stride()} are neither row- nor column-major")
     bias_ptr, bias_type, stride_bias = _bias(bias, groups, N, True)
-    at, bt, ct = _torch_dtype_name(A), _torch_dtype_name(B), _torch_dtype_name(C)
-    desc = DgGroupedDesc(_GROUPED_SIZE, DG_RAGGED_M, _DTYPE[at], _DTYPE[bt], _DTYPE[ct],
-                         _DTYPE[bias_type], _ORDER[order], _enum(_ACT, act), groups, rows, 0, N, K,
-                         _row_ld(A, "A"), ldb, _row_ld(C, "C"), sb, 0, stride_bias, alpha, beta,
+    desc = DgGroupedDesc(_GROUPED_SIZE, DG_RAGGED_M, _code(A), _code(B), _code(C), bias_type, order,
+                         _enum(_ACT, act), groups, rows, 0, N, K, _row_ld(rows, K, *A.stride(), "A"),
+                         ldb, _row_ld(rows, N, *C.stride(), "C"), sb, 0, stride_bias, alpha, beta,
                          bias_ptr)
-    _on_stream(A, stream, lambda s: dg_gemm_grouped(desc, A.data_ptr(), B.data_ptr(), C.data_ptr(),
-                                                    offsets.data_ptr(), s))
+    _launch(_entry().dg_gemm_grouped, "dg_gemm_grouped", device, stream, desc, A.data_ptr(),
+            B.data_ptr(), C.data_ptr(), offsets.data_ptr())
     return C
 
 
@@ -229,20 +246,24 @@ def gemm_grouped_k(A, B, offsets, C=None, *, alpha=1.0, beta=0.0, out_dtype=None
     A: (M, rows), column-major (X is (rows, M) row-major).  B: (rows, N),
     row-major.  offsets as in gemm_grouped.  Returns C (groups, M, N); an
     empty group's is beta * C[e], or zeros."""
-    if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[0]:
-        raise ValueError(f"A {tuple(A.shape)} and B {tuple(B.shape)}: (M, rows) and (rows, N) are wanted")
+    ashape, bshape = A.shape, B.shape
+    if len(ashape) != 2 or len(bshape) != 2 or ashape[1] != bshape[0]:
+        raise ValueError(f"A {tuple(ashape)} and B {tuple(bshape)}: (M, rows) and (rows, N) are wanted")
     if offsets.dim() != 1 or offsets.numel() < 1:
         raise ValueError("offsets: an int32 tensor of groups + 1 entries is wanted")
-    (M, rows), N, groups = A.shape, B.shape[1], offsets.numel() - 1
+    (M, rows), N, groups = ashape, bshape[1], offsets.numel() - 1
     _check_offsets(offsets, groups)
     C = _output(C, (groups, M, N), out_dtype, A, beta)
-    _same_device(A, B=B, C=C, offsets=offsets)
-    at, bt, ct = _torch_dtype_name(A), _torch_dtype_name(B), _torch_dtype_name(C)
-    desc = DgGroupedDesc(_GROUPED_SIZE, DG_RAGGED_K, _DTYPE[at], _DTYPE[bt], _DTYPE[ct], 0,
-                         DG_ROW_MAJOR, 0, groups, rows, M, N, 0, _row_ld(A.t(), "A transposed"),
-                         _row_ld(B, "B"), _row_ld(C, "C"), 0, C.stride(0), 0, alpha, beta, None)
-    _on_stream(A, stream, lambda s: dg_gemm_grouped(desc, A.data_ptr(), B.data_ptr(), C.data_ptr(),
-                                                    offsets.data_ptr(), s))
+    device = A.get_device()
+    _same_device(device, B=B, C=C, offsets=offsets)
+    sm, sr = A.stride()
+    sc, cr, cc = C.stride()
+    desc = DgGroupedDesc(_GROUPED_SIZE, DG_RAGGED_K, _code(A), _code(B), _code(C), DG_F32,
+                         DG_ROW_MAJOR, 0, groups, rows, M, N, 0,
+                         _row_ld(rows, M, sr, sm, "A transposed"), _row_ld(rows, N, *B.stride(), "B"),
+                         _row_ld(M, N, cr, cc, "C"), 0, sc, 0, alpha, beta, None)
+    _launch(_entry().dg_gemm_grouped, "dg_gemm_grouped", device, stream, desc, A.data_ptr(),
+            B.data_ptr(), C.data_ptr(), offsets.data_ptr())
     return C
 
 
@@ -258,34 +279,37 @@ def gemm_qweight(A, Q, scales, zeros=None, C=None, *, group_size, offsets=None, 
     zeros and optionally bias have a leading dimension of groups, and each
     row of A uses its group's weights; rows of no group are left alone."""
     import torch
+    ashape, qshape, sshape = A.shape, Q.shape, scales.shape
     grouped = offsets is not None
-    lead = 1 if grouped else 0
-    if A.dim() != 2 or Q.dim() != 2 + lead or scales.dim() != 2 + lead or group_size < 1:
+    dims = 3 if grouped else 2
+    if len(ashape) != 2 or len(qshape) != dims or len(sshape) != dims or group_size < 1:
         raise ValueError("A (M, K), Q ([groups,] N, ceil(K / 2)) and scales ([groups,] N, "
                          "ceil(K / group_size)) are wanted")
-    (M, K), N = A.shape, Q.shape[-2]
-    groups = Q.shape[0] if grouped else 1
-    per_row = -(-K // group_size)
-    if Q.dtype != torch.uint8 or Q.shape[-1] != -(-K // 2):
-        raise ValueError(f"Q: uint8 rows of {-(-K // 2)} bytes are wanted")
-    if tuple(scales.shape) != ((groups, N, per_row) if grouped else (N, per_row)):
-        raise ValueError(f"scales: shape {tuple(scales.shape)} for {N} rows of {per_row} groups")
-    if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != scales.shape or
-                              zeros.stride() != scales.stride()):
+    M, K = ashape
+    N, per_row = qshape[-2], -(-K // group_size)
+    if Q.dtype != torch.uint8 or qshape[-1] != (K + 1) // 2:
+        raise ValueError(f"Q: uint8 rows of {(K + 1) // 2} bytes are wanted")
+    if sshape[-1] != per_row or sshape[:-1] != qshape[:-1]:
+        raise ValueError(f"scales: shape {tuple(sshape)} for {N} rows of {per_row} groups")
+    qstride, sstride = Q.stride(), scales.stride()
+    if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != sshape or
+                              zeros.stride() != sstride):
         raise ValueError("zeros: uint8 with the shape and strides of scales is wanted")
+    groups = stride_q = stride_s = 0
     if grouped:
+        groups, stride_q, stride_s = qshape[0], qstride[0], sstride[0]
         _check_offsets(offsets, groups)
     C = _output(C, (M, N), out_dtype, A, beta)
-    _same_device(A, Q=Q, scales=scales, zeros=zeros, C=C, offsets=offsets, bias=bias)
+    device = A.get_device()
+    _same_device(device, Q=Q, scales=scales, zeros=zeros, C=C, offsets=offsets, bias=bias)
     bias_ptr, bias_type, stride_bias = _bias(bias, groups, N, grouped)
-    at, ct, st = _torch_dtype_name(A), _torch_dtype_name(C), _torch_dtype_name(scales)
-    desc = DgQweightDesc(_QWEIGHT_SIZE, _DTYPE[at], _DTYPE[ct], _DTYPE[st], _DTYPE[bias_type],
-                         _enum(_ACT, act), groups, M, N, K, group_size, _row_ld(A, "A"),
-                         _row_ld(C, "C"), _row_ld(Q, "Q"), _row_ld(scales, "scales"),
-                         Q.stride(0) if grouped else 0, scales.stride(0) if grouped else 0,
+    desc = DgQweightDesc(_QWEIGHT_SIZE, _code(A), _code(C), _code(scales), bias_type,
+                         _enum(_ACT, act), groups if grouped else 1, M, N, K, group_size,
+                         _row_ld(M, K, *A.stride(), "A"), _row_ld(M, N, *C.stride(), "C"),
+                         _row_ld(N, qshape[-1], *qstride[-2:], "Q"),
+                         _row_ld(N, per_row, *sstride[-2:], "scales"), stride_q, stride_s,
                          stride_bias, alpha, beta, bias_ptr)
-    _on_stream(A, stream, lambda s: dg_gemm_qweight(
-        desc, A.data_ptr(), Q.data_ptr(), scales.data_ptr(),
-        zeros.data_ptr() if zeros is not None else None, C.data_ptr(),
-        offsets.data_ptr() if grouped else None, s))
+    _launch(_entry().dg_gemm_qweight, "dg_gemm_qweight", device, stream, desc, A.data_ptr(),
+            Q.data_ptr(), scales.data_ptr(), None if zeros is None else zeros.data_ptr(),
+            C.data_ptr(), offsets.data_ptr() if grouped else None)
     return C
