@@ -51,10 +51,13 @@ SOURCES = [
     "kernel_grouped_generic.hip",
     "kernel_grouped16_m256.hip",
     "kernel_grouped16_m128.hip",
+    "kernel_grouped16_m128x64.hip",
     "kernel_grouped16_k256.hip",
     "kernel_grouped16_k128.hip",
-    "kernel_stream16.hip",
+    "kernel_grouped_f32.hip",
+    "kernel_stream.hip",
     "kernel_qstream.hip",
+    "kernel_qtile.hip",
 ]
 
 

@@ -206,14 +206,19 @@ hipError_t launch_grouped_generic(const GroupedArgs &a, bool ragged_k, uint32_t 
                                   hipStream_t s);
 // 16-bit matrix-core tiles (256 x 256 and 128 x 128)
 hipError_t launch_grouped16_m256(const GroupedArgs &a, uint32_t programs, hipStream_t s);
+hipError_t launch_grouped16_m128x64(const GroupedArgs &a, uint32_t programs, hipStream_t s);
 hipError_t launch_grouped16_m128(const GroupedArgs &a, uint32_t programs, hipStream_t s);
 hipError_t launch_grouped16_k256(const GroupedArgs &a, uint32_t programs, hipStream_t s);
 hipError_t launch_grouped16_k128(const GroupedArgs &a, uint32_t programs, hipStream_t s);
-// few rows per group (kernel_stream16.hip)
+// fp32 matrix-core tile (128 x 128)
+hipError_t launch_grouped_f32_m(const GroupedArgs &a, uint32_t programs, hipStream_t s);
+hipError_t launch_grouped_f32_k(const GroupedArgs &a, uint32_t programs, hipStream_t s);
+// few rows per group (kernel_stream.hip)
 hipError_t launch_grouped_stream(int32_t variant, const GroupedArgs &a, uint32_t programs,
                                  hipStream_t s);
-hipError_t launch_qweight_stream(int32_t variant, const QweightArgs &a, uint32_t programs,
-                                 hipStream_t s);
+hipError_t launch_qweight_rows(int32_t variant, const QweightArgs &a, uint32_t programs,
+                               hipStream_t s);
+hipError_t launch_qweight_tile(const QweightArgs &a, uint32_t programs, hipStream_t s);
 hipError_t launch_qweight_generic(const QweightArgs &a, uint32_t programs, hipStream_t s);
 
 constexpr int kGroupedGenericTile = 64;

@@ -150,11 +150,15 @@ const GroupedKernel kTile256 = {"mfma16_256x256", 256, 256, launch_grouped16_m25
                                 launch_grouped16_k256};
 const GroupedKernel kTile128 = {"mfma16_128x128", 128, 128, launch_grouped16_m128,
                                 launch_grouped16_k128};
-const GroupedKernel kStream16x32 = {"stream16_16x32", 16, 32, stream_m<0>, nullptr};
-const GroupedKernel kStream16x64 = {"stream16_16x64", 16, 64, stream_m<1>, nullptr};
-const GroupedKernel kStream32x64 = {"stream16_32x64", 32, 64, stream_m<2>, nullptr};
-const GroupedKernel *const kGrouped16[] = {&kTile256, &kTile128, &kStream16x32, &kStream16x64,
-                                           &kStream32x64};
+const GroupedKernel kTile128x64 = {"mfma16_128x128x64", 128, 128, launch_grouped16_m128x64, nullptr};
+const GroupedKernel kTileF32 = {"mfma_f32_128x128", 128, 128, launch_grouped_f32_m,
+                                launch_grouped_f32_k};
+const GroupedKernel kStream16x32 = {"stream_16x32", 16, 32, stream_m<0>, nullptr};
+const GroupedKernel kStream16x64 = {"stream_16x64", 16, 64, stream_m<1>, nullptr};
+const GroupedKernel kStream32x64 = {"stream_32x64", 32, 64, stream_m<2>, nullptr};
+const GroupedKernel *const kGrouped16[] = {&kTile256,     &kTile128,     &kTile128x64,
+                                           &kStream16x32, &kStream16x64, &kStream32x64};
+const GroupedKernel *const kGroupedF32[] = {&kTileF32, &kStream16x32, &kStream16x64, &kStream32x64};
 
 // The kernel of `table` that DG_FORCE_GROUPED names (benchmarking and
 // tests), or NULL.
@@ -173,13 +177,14 @@ struct GroupedPlan {
     uint32_t programs;
 };
 
-// The 16-bit matrix-core tiles read whole 16-byte pieces of rows and
-// address a tile with 32-bit byte offsets.
-bool mfma16_ok(const dg_grouped_desc *d, const void *A, const void *B)
+// The matrix-core kernels read whole 16-byte pieces of rows; the 16-bit
+// tiles address a tile with 32-bit byte offsets.
+bool mfma_ok(const dg_grouped_desc *d, const void *A, const void *B)
 {
-    return d->a_type != DG_F32 && aligned_to(A, 16) && aligned_to(B, 16) && d->lda % 8 == 0 &&
-           d->ldb % 8 == 0 && d->lda < (1 << 22) && d->ldb < (1 << 22) &&
-           (d->ragged == DG_RAGGED_K || d->groups <= 1 || d->stride_b % 8 == 0);
+    const int64_t n = d->a_type == DG_F32 ? 4 : 8;
+    return aligned_to(A, 16) && aligned_to(B, 16) && d->lda % n == 0 && d->ldb % n == 0 &&
+           d->lda < (1 << 22) && d->ldb < (1 << 22) &&
+           (d->ragged == DG_RAGGED_K || d->groups <= 1 || d->stride_b % n == 0);
 }
 
 // The kernel for a problem.  Group lengths are unknown; the mean stands for
@@ -194,23 +199,32 @@ bool mfma16_ok(const dg_grouped_desc *d, const void *A, const void *B)
 //   up to 16, the 32-row one: 1024 rows on those 64 groups 105 against
 //     112-120 on 16 rows, 4 groups, 64 rows, 4096 x 4096 31-34 against 43
 //     and 40-51 on the tile;
-//   above, a tile: the whole waves of 256 workgroups that each would make,
-//     at 1 a wave for 256 x 256 (one workgroup per CU) and 0.72 for 512
-//     workgroups of 128 x 128, half a wave added for their last one (8192
-//     rows, 16 groups, 4096 x 4096: 326 against 390; 4096 rows, 32 groups,
-//     2048 x 2048: 113 against 81).
+//   fp32 keeps the 32-row one below 1024 tiles of 128 x 128 (1000 rows, 5
+//     groups, 512 x 260: 10 against 63; 4096 rows, 16 groups, 2048 x 2048:
+//     332-390 against 393-407) and takes the tile above (8192 rows, 2048 x
+//     4096: 1151-1166 against 1228-1440);
+//   above, 16 bits, a tile.  Below 128 rows the 128 x 128 one with a deep
+//     ring (1000 rows, 20 groups, 1024 x 4096: 36 against 40 on the one with
+//     64-deep stages); else the cheaper of 256 x 256 and 128 x 128 with
+//     64-deep stages, in whole waves of 256 workgroups for the first (one per
+//     CU) and waves of 512, plus half a one for the last, at 0.64 of the cost
+//     for the second, each costing its K and about 450 k of start and
+//     epilogue (8192 rows, 16 groups, 4096 x 4096: 326 against 347; 4095
+//     rows, 7 groups, 1000 x 4097: 78 against 66).
 // Ragged K: the 128 x 128 tile, whose second workgroup on a CU covers the
 // other's epilogue (16 groups of 2048 x 2048, 8192 rows: 103 against 107;
 // 32 of 512 x 1024: 18-21 against 24), unless the groups are long and 256 x
 // 256 tiles fill the chip (8 of 1024 x 2048: 47 against 50).
 const GroupedKernel *choose(const dg_grouped_desc *d, const void *A, const void *B)
 {
-    if (!mfma16_ok(d, A, B))
+    if (!mfma_ok(d, A, B))
         return &kGeneric;
-    const bool rk = d->ragged == DG_RAGGED_K;
-    if (const GroupedKernel *k = forced_kernel(kGrouped16))
+    const bool rk = d->ragged == DG_RAGGED_K, f32 = d->a_type == DG_F32;
+    if (const GroupedKernel *k = f32 ? forced_kernel(kGroupedF32) : forced_kernel(kGrouped16))
         if (rk ? k->ragged_k : k->ragged_m)
             return k;
+    if (f32 && rk)
+        return &kTileF32;
     const double mean = (double)d->rows / (double)d->groups;
     const double n256 = (double)ceil_div(d->N, 256), n128 = (double)ceil_div(d->N, 128);
     if (rk) {
@@ -222,10 +236,15 @@ const GroupedKernel *choose(const dg_grouped_desc *d, const void *A, const void 
                                                                             : &kStream16x64;
     if (mean <= 16)
         return &kStream32x64;
-    const double lost = 0.6 * (double)d->groups;
+    if (f32)
+        return row_tiles(d->rows, d->groups, 128) * ceil_div(d->N, 128) < 4 * kCus ? &kStream32x64
+                                                                                   : &kTileF32;
+    if (mean < 128)
+        return &kTile128;
+    const double lost = 0.6 * (double)d->groups, k = (double)d->K;
     const double waves256 = ceil(((double)d->rows / 256 + lost) * n256 / kCus);
     const double waves128 = ((double)d->rows / 128 + lost) * n128 / (2 * kCus) + 0.5;
-    return waves256 < 0.72 * waves128 ? &kTile256 : &kTile128;
+    return waves256 * (k + 490) < 0.64 * waves128 * (k + 400) ? &kTile256 : &kTile128x64;
 }
 
 dg_status make_plan(const dg_grouped_desc *d, const void *A, const void *B, GroupedPlan *p)
@@ -294,19 +313,21 @@ struct QweightKernel {
 };
 
 template <int V>
-hipError_t qstream(const QweightArgs &a, uint32_t p, hipStream_t s)
+hipError_t qrows(const QweightArgs &a, uint32_t p, hipStream_t s)
 {
-    return launch_qweight_stream(V, a, p, s);
+    return launch_qweight_rows(V, a, p, s);
 }
-
 const QweightKernel kQGeneric = {"generic", kGroupedGenericTile, kGroupedGenericTile,
                                  launch_qweight_generic};
-const QweightKernel kQ16x16 = {"qstream_16x16", 16, 16, qstream<0>};
-const QweightKernel kQ16x32 = {"qstream_16x32", 16, 32, qstream<1>};
-const QweightKernel kQ16x64 = {"qstream_16x64", 16, 64, qstream<2>};
-const QweightKernel kQ32x32 = {"qstream_32x32", 32, 32, qstream<3>};
-const QweightKernel kQ32x64 = {"qstream_32x64", 32, 64, qstream<4>};
-const QweightKernel *const kQweight[] = {&kQ32x64, &kQ32x32, &kQ16x64, &kQ16x32, &kQ16x16};
+const QweightKernel kQ4x16 = {"qstream_4x16", 16, 16, qrows<0>};   // at most 4 rows
+const QweightKernel kQ16x16 = {"qstream_16x16", 16, 16, qrows<1>};
+const QweightKernel kQ16x32 = {"qstream_16x32", 16, 32, qrows<2>};
+const QweightKernel kQ16x64 = {"qstream_16x64", 16, 64, qrows<3>};
+const QweightKernel kQ32x32 = {"qstream_32x32", 32, 32, qrows<4>};
+const QweightKernel kQ32x64 = {"qstream_32x64", 32, 64, qrows<5>};
+const QweightKernel kQ64x256 = {"qtile_64x256", 64, 256, launch_qweight_tile};
+const QweightKernel *const kQweight[] = {&kQ64x256, &kQ32x64, &kQ32x32, &kQ16x64,
+                                         &kQ16x32,  &kQ16x16};
 
 struct QweightPlan {
     const QweightKernel *kernel;
@@ -327,26 +348,33 @@ int64_t row_tiles(const dg_qweight_desc *d, bool offsets, const QweightKernel &k
     return offsets ? row_tiles(d->M, d->groups, k.bm) : ceil_div(d->M, k.bm);
 }
 
-// 32 rows where a group has more than 16, and the widest workgroup (each
-// reads A once) that still makes 512 of them for up to 4 rows, 256 for
-// more, where A's traffic counts (us, bf16, group size 128):
+// From 512 rows a group, if 64 x 256 tiles fill the chip, the tile (us, 4096
+// x 4096, bf16, group size 128): 1024 rows 55 against 94, 2048 rows 115
+// against 187; below, it does not (256 rows: 54 against 25).
+// Else 32 rows where a group has more than 16, and the widest workgroup
+// (each reads A once) that still makes 512 of them for up to 4 rows, 256
+// for more, where A's traffic counts:
 //   1 row,   4096 x 4096: 5.4 on 16 columns, 6.9 on 32, 10.4 on 64;
 //            16384 x 4096: 12.5, 10.2, 11.8;  8192 x 8192: 10.5, 12.6, 19.1
 //   16 rows, 4096 x 4096: 7.2, 9.2, 11.8;  16384 x 4096: 18.6, 14.0, 13.3
 //   64 rows, 16384 x 4096: 31.8 on 16 x 64, 31.6 on 32 x 32, 26.9 on 32 x 64
+// 16 columns of up to 4 rows take panels of twice the K, in which most K
+// are one panel.
 const QweightKernel *choose(const dg_qweight_desc *d, bool offsets, const void *A, const void *Q)
 {
     if (!qstream_ok(d, offsets, A, Q))
         return &kQGeneric;
+    const bool few = !offsets && d->M <= 4;
     if (const QweightKernel *k = forced_kernel(kQweight))
         return k;
     const int64_t rows = offsets ? d->M / d->groups : d->M;
     const int64_t want = rows <= 4 ? 512 : 256;
-    for (const QweightKernel *k : kQweight)
-        if ((k->bm == 16 || rows > 16) &&
-            ceil_div(d->N, k->bn) >= ceil_div(want, row_tiles(d, offsets, *k)))
+    for (const QweightKernel *k : kQweight) {
+        const bool rows_fit = k->bm == 64 ? rows >= 512 : k->bm == 32 ? rows > 16 : k->bm == 16;
+        if (rows_fit && ceil_div(d->N, k->bn) >= ceil_div(want, row_tiles(d, offsets, *k)))
             return k;
-    return &kQ16x16;
+    }
+    return few ? &kQ4x16 : &kQ16x16;
 }
 
 dg_status make_plan(const dg_qweight_desc *d, bool offsets, const void *A, const void *Q,

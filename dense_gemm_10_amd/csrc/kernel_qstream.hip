@@ -1,404 +1,18 @@
-// Products with 4-bit weights (stream.hpp): W's codes go from memory into
-// registers 16 bytes per lane, become MFMA operands by two instructions per
-// pair of weights, and the scales multiply fp32 sums.
-//
-// Codes to operands.  A 16-bit float with exponent 4 and the code q in its
-// top four fraction bits is 16 + q, exactly: bf16 0x4180 | q << 3, fp16
-// 0x4c00 | q << 6.  One shift and one and-or of a word of eight codes give
-// codes j and j + 4 as the two halves of a register, so the operand's
-// k-order is 0 4 1 5 2 6 3 7; A is staged in LDS in the same order.  With U
-// = sum a (16 + q) and S = sum a over the k of one scale (S by one more
-// MFMA, against a column of ones), both in fp32,
-//   sum a scale (q - zero) = scale (U - (16 + zero) S).
-// Nothing is rounded to 16 bits; the subtraction costs the sums at most
-// five bits of fp32 (|16 + q| <= 31 against |q - zero| of a few units).
-//
-// Work split.  A workgroup is NW x KW wavefronts and owns 16 FM rows x 16
-// FN NW columns; it walks K in panels of 128 KW TS.  Per panel the
-// workgroup stages A's rows and the panel's scales in LDS, and wavefront
-// (n, w) takes its 16 FN columns over the steps w, w + KW, ... of 128 k.
-// The next panel's codes, A and scales are loaded into registers before
-// this panel is multiplied, so memory is never waited for in the loop.
-// A through LDS and not straight into registers: there each wavefront's A
-// pieces take four times the load instructions of its codes, and the
-// vector-memory path, not HBM, bounds the kernel (16384 x 8192, one row: 31
-// us; 16 rows: 46 us).
-//
-// Codes to MFMA steps.  Lane 16 g + c loads codes 32 g .. 32 g + 31 of row
-// c, 64 bytes of each row, and a 4 x 4 exchange between the four 16-lane
-// groups (two half-wave swaps, two quarter swaps) gives register t of group
-// g the codes 32 t + 8 g .. + 7: MFMA t of the step then covers 32
-// consecutive k, which share a scale for any group size that is a multiple
-// of 32.  SPG: MFMA steps that surely share a scale (1, 2 or 4: group sizes
-// that are multiples of 32, 64 or 128).
-#include "stream.hpp"
+// Instantiations of the products with 4-bit weights (qstream.hpp): few rows.
+#include "qstream.hpp"
 
 namespace dg {
 
-namespace {
-
-constexpr int QK = 128;            // k of one step of a wavefront
-
-// Exchange between the two registers: lanes 32-63 of x with lanes 0-31 of y.
-__device__ __forceinline__ void swap_halves(uint32_t &x, uint32_t &y)
-{
-    const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
-    x = r[0];
-    y = r[1];
-}
-// Lanes 16-31 of x with lanes 0-15 of y, and 48-63 of x with 32-47 of y.
-__device__ __forceinline__ void swap_quarters(uint32_t &x, uint32_t &y)
-{
-    const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
-    x = r[0];
-    y = r[1];
-}
-
-// w[t] of lane group g becomes w[g] of lane group t.
-__device__ __forceinline__ void transpose_groups(uint32_t (&w)[4])
-{
-    swap_halves(w[0], w[2]);
-    swap_halves(w[1], w[3]);
-    swap_quarters(w[0], w[1]);
-    swap_quarters(w[2], w[3]);
-}
-
-// 16.0 in both halves of a register, opaque to the compiler: an and-or takes
-// its mask and one more constant only if one of them is in a vector register.
-template <int T>
-__device__ __forceinline__ uint32_t sixteen()
-{
-    uint32_t v = T == DT_F16 ? 0x4c004c00u : 0x41804180u;
-    asm("" : "+v"(v));
-    return v;
-}
-
-// Eight codes of a word as an operand of values 16 + q, in k-order 0 4 1 5
-// 2 6 3 7.
-template <int T>
-__device__ __forceinline__ uint4 codes_to_operand(uint32_t w, uint32_t base)
-{
-    constexpr uint32_t mask = T == DT_F16 ? 0x03c003c0u : 0x00780078u;
-    if constexpr (T == DT_F16)
-        return make_uint4((w << 6 & mask) | base, (w << 2 & mask) | base, (w >> 2 & mask) | base,
-                          (w >> 6 & mask) | base);
-    else
-        return make_uint4((w << 3 & mask) | base, (w >> 1 & mask) | base, (w >> 5 & mask) | base,
-                          (w >> 9 & mask) | base);
-}
-
-// Eight consecutive 16-bit values of A in the same order.
-__device__ __forceinline__ uint4 reorder_a(uint4 v)
-{
-    return make_uint4(__builtin_amdgcn_perm(v.z, v.x, 0x05040100u),
-                      __builtin_amdgcn_perm(v.z, v.x, 0x07060302u),
-                      __builtin_amdgcn_perm(v.w, v.y, 0x05040100u),
-                      __builtin_amdgcn_perm(v.w, v.y, 0x07060302u));
-}
-
-// LDS of a workgroup: A's panel, rows 16 bytes apart in banks, and the
-// panel's (scale, -(16 + zero)) pairs; or the wavefronts' sums at the end.
-template <int SPG, int FM, int FN, int NW, int KW, int TS>
-struct QPanel {
-    static constexpr int K = QK * KW * TS;            // k of a panel
-    static constexpr int E = K / (32 * SPG);          // scales of a row
-    static constexpr int COLS = 16 * FN * NW;
-    static constexpr int NT = 64 * NW * KW;
-    static constexpr int A_LD = K + 8;                // 16-bit elements
-    static constexpr int S_LD = E + 1;                // float pairs
-    static constexpr int A_BYTES = 16 * FM * A_LD * 2;
-    static constexpr int A_PER = 16 * FM * K / 8 / NT;    // 16-byte pieces of A per thread
-    static constexpr int S_ALL = COLS * E;                // scales of the panel
-    static constexpr int S_PER = (S_ALL + NT - 1) / NT;   // ... per thread
-    static constexpr int SUM_LD = COLS + 4;
-    static constexpr int LOOP = A_BYTES + COLS * S_LD * 8;
-    static constexpr int STORE = KW * 16 * FM * SUM_LD * 4;
-    static constexpr int BYTES = LOOP > STORE ? LOOP : STORE;
-    static_assert(A_PER * NT * 8 == 16 * FM * K, "A split");
-};
-
-template <int T, bool S32, bool ZEROS, int SPG, int FM, int FN, int NW, int KW, int TS>
-__global__ __launch_bounds__(64 * NW * KW) __attribute__((amdgpu_waves_per_eu(4)))
-void qweight_stream_kernel(QweightArgs a, FastDiv by_group)
-{
-    using frag_t = typename frag_of<T>::type;
-    using P = QPanel<SPG, FM, FN, NW, KW, TS>;
-    extern __shared__ uint4 lds[];
-    GroupTile t;
-    if (a.offsets) {
-        t = find_group_tile<16 * FM, 16>(a.offsets, a.groups, a.rows, a.tiles_n, blockIdx.x);
-        if (t.group < 0)
-            return;
-    } else {
-        // column tile by column tile, the row tiles of one (which read the
-        // same codes) together, dealt to the XCDs in contiguous runs
-        const uint32_t tm = ((uint32_t)a.rows + 16 * FM - 1) / (16 * FM);
-        const uint32_t N = tm * a.tiles_n, x = blockIdx.x % kNumXcd, r = N % kNumXcd;
-        const uint32_t L = x * (N / kNumXcd) + (x < r ? x : r) + blockIdx.x / kNumXcd;
-        t = GroupTile{0, 0, a.rows, L % tm, L / tm};
-    }
-    const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, kg = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int nw = wave % NW, kw = wave / NW;
-    const int64_t m0 = (int64_t)t.row_tile * (16 * FM), n0 = (int64_t)t.col_tile * P::COLS;
-    const int rows = (int)(t.rows - m0 < 16 * FM ? t.rows - m0 : 16 * FM);
-    const int cols = (int)(a.N - n0 < P::COLS ? a.N - n0 : P::COLS);
-
-    // Each operand: a uniform base and a 32-bit byte offset per lane
-    // (checked on the host to fit).  Columns past the last repeat it.
-    const global_base ab = uniform_base((const uint16_t *)a.A + (t.start + m0) * a.lda);
-    const global_base qb = uniform_base(a.Q + t.group * a.stride_q + n0 * a.ldq);
-    const int64_t s0 = t.group * a.stride_s + n0 * a.lds;
-    const global_base sb = uniform_base((const char *)a.scales + s0 * (S32 ? 4 : 2));
-    const global_base zb = uniform_base(a.zeros + (ZEROS ? s0 : 0));
-    const uint32_t K = (uint32_t)a.K;      // a multiple of 32 below 2^31 (checked on the host)
-    uint32_t qo[FN];
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-        const uint32_t n = 16 * (FN * nw + j) + c;
-        qo[j] = (n < (uint32_t)cols ? n : cols - 1) * (uint32_t)a.ldq;
-    }
-    uint16_t *a_lds = (uint16_t *)lds;
-    float2 *s_lds = (float2 *)((char *)lds + P::A_BYTES);
-
-    struct Codes {
-        uint4 q[TS][FN];
-    };
-    struct Staged {
-        uint4 a[P::A_PER];
-        uint32_t s[P::S_PER];
-        uint32_t z[P::S_PER];
-    };
-    // k past K reads the row's last codes: A is zero there.
-    auto load_codes = [&](Codes &r, uint32_t k0) {
-#pragma unroll
-        for (int i = 0; i < TS; ++i) {
-            const uint32_t k = k0 + (kw + i * KW) * QK + 32 * kg;
-            const uint32_t at = (k < K ? k : K - 32) / 2;
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-                r.q[i][j] = load16_at(qb, qo[j] + at);
-        }
-    };
-    auto load_panel = [&](Staged &r, uint32_t k0) {
-#pragma unroll
-        for (int i = 0; i < P::A_PER; ++i) {
-            const int piece = tid + i * P::NT, row = piece / (P::K / 8);
-            const uint32_t k = k0 + piece % (P::K / 8) * 8;
-            if (row < rows)
-                r.a[i] = load16_at(ab, (uint32_t)row * (uint32_t)(2 * a.lda) + 2 * (k < K ? k : 0));
-        }
-#pragma unroll
-        for (int i = 0; i < P::S_PER; ++i) {
-            const int all = tid + i * P::NT, e = all < P::S_ALL ? all : P::S_ALL - 1;
-            const int n = e / P::E;
-            const uint32_t k = k0 + e % P::E * (32 * SPG);
-            const uint32_t at = (uint32_t)(n < cols ? n : cols - 1) * (uint32_t)a.lds +
-                                fastdiv(k < K ? k : K - 1, by_group);
-            r.s[i] = S32 ? load_at<uint32_t>(sb, at * 4) : load_at<uint16_t>(sb, at * 2);
-            if (ZEROS)
-                r.z[i] = load_at<uint8_t>(zb, at);
-        }
-    };
-    const bool f16_scale = a.scale_type == DT_F16;
-    auto store_panel = [&](const Staged &r, uint32_t k0) {
-#pragma unroll
-        for (int i = 0; i < P::A_PER; ++i) {
-            const int piece = tid + i * P::NT, row = piece / (P::K / 8), at = piece % (P::K / 8) * 8;
-            if (row < rows)
-                *(uint4 *)(a_lds + row * P::A_LD + at) =
-                    k0 + at < K ? reorder_a(r.a[i]) : make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-        for (int i = 0; i < P::S_PER; ++i) {
-            const int e = tid + i * P::NT;
-            float f = __uint_as_float(r.s[i]);
-            if (!S32)
-                f = f16_scale ? f16_to_f32((uint16_t)r.s[i]) : bf16_to_f32((uint16_t)r.s[i]);
-            const float h = ZEROS ? -16.0f - (float)(r.z[i] & 15) : -24.0f;
-            // past K a scale of zero: the sums there are zero, whatever the scale
-            const bool in = k0 + e % P::E * (32 * SPG) < K;
-            if (e < P::S_ALL)
-                s_lds[e / P::E * P::S_LD + e % P::E] = make_float2(in ? f : 0.0f, h);
-        }
-    };
-
-    const f32x4_t none{0.0f, 0.0f, 0.0f, 0.0f};
-    const uint32_t base = sixteen<T>();
-    const uint32_t one2 = T == DT_F16 ? 0x3c003c00u : 0x3f803f80u;
-    const frag_t ones = __builtin_bit_cast(frag_t, make_uint4(one2, one2, one2, one2));
-    f32x4_t acc[FM][FN];
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-            acc[i][j] = none;
-    const uint16_t *a_row[FM];             // rows past the last repeat it
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-        a_row[i] = a_lds + (16 * i + c < rows ? 16 * i + c : rows - 1) * P::A_LD + 8 * kg;
-    const float2 *s_row = s_lds + (16 * FN * nw + c) * P::S_LD;
-
-    auto multiply = [&](const Codes &r) {
-#pragma unroll
-        for (int i = 0; i < TS; ++i) {
-            const int step = kw + i * KW;          // of the panel
-            sched_fence();                         // one step's operands in registers at a time
-            uint32_t w[FN][4];
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                w[j][0] = r.q[i][j].x;
-                w[j][1] = r.q[i][j].y;
-                w[j][2] = r.q[i][j].z;
-                w[j][3] = r.q[i][j].w;
-                transpose_groups(w[j]);
-            }
-            f32x4_t u[FM][FN], sum[FM];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const bool first = m % SPG == 0;
-                frag_t af[FM];
-#pragma unroll
-                for (int x = 0; x < FM; ++x) {
-                    af[x] = *(const frag_t *)(a_row[x] + step * QK + 32 * m);
-                    sum[x] = mfma_16x16x32(af[x], ones, first ? none : sum[x]);
-                }
-#pragma unroll
-                for (int j = 0; j < FN; ++j) {
-                    const frag_t b = __builtin_bit_cast(frag_t, codes_to_operand<T>(w[j][m], base));
-#pragma unroll
-                    for (int x = 0; x < FM; ++x)
-                        u[x][j] = mfma_16x16x32(af[x], b, first ? none : u[x][j]);
-                }
-                if (m % SPG == SPG - 1) {
-                    sched_fence();
-#pragma unroll
-                    for (int j = 0; j < FN; ++j) {
-                        const float2 s = s_row[j * 16 * P::S_LD + step * (4 / SPG) + m / SPG];
-#pragma unroll
-                        for (int x = 0; x < FM; ++x)
-#pragma unroll
-                            for (int v = 0; v < 4; ++v)
-                                acc[x][j][v] = fmaf(s.x, fmaf(s.y, sum[x][v], u[x][j][v]), acc[x][j][v]);
-                        // finished here: otherwise the compiler puts these additions off past
-                        // the barrier and keeps every u and sum until then
-#pragma unroll
-                        for (int x = 0; x < FM; ++x)
-                            asm volatile("" : "+v"(acc[x][j]));
-                    }
-                }
-            }
-        }
-    };
-
-    if (a.alpha != 0.0f && K > 0) {
-        Codes now, next;
-        Staged panel;
-        load_codes(now, 0);
-        load_panel(panel, 0);
-        store_panel(panel, 0);
-        lds_barrier();
-        for (uint32_t k0 = 0;;) {
-            const uint32_t k1 = k0 + P::K;
-            if (k1 >= K) {
-                multiply(now);
-                break;
-            }
-            load_panel(panel, k1);
-            load_codes(next, k1);
-            multiply(now);
-            lds_barrier();                 // every wavefront is done with this panel
-            store_panel(panel, k1);
-            lds_barrier();
-            now = next;
-            k0 = k1;
-        }
-        lds_barrier();
-    }
-
-    // the KW wavefronts' sums, added in wavefront order, and the epilogue
-    GemmArgs g{};
-    g.M = t.rows;
-    g.N = a.N;
-    g.ldc = a.ldc;
-    g.alpha = a.alpha;
-    g.beta = a.beta;
-    g.act = a.act;
-    g.c_type = a.c_type;
-    g.bias_type = a.bias_type;
-    g.C = (char *)a.C + (int64_t)t.start * a.ldc * (a.c_type == DT_F32 ? 4 : 2);
-    g.bias = a.bias ? (const char *)a.bias + t.group * a.stride_bias * (a.bias_type == DT_F32 ? 4 : 2)
-                    : nullptr;
-    float *sums = (float *)lds;
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-                sums[(kw * 16 * FM + 16 * i + 4 * kg + v) * P::SUM_LD + 16 * (FN * nw + j) + c] =
-                    acc[i][j][v];
-    lds_barrier();
-    for (int o = tid; o < 16 * FM * P::COLS; o += P::NT) {
-        const int r = o / P::COLS, n = o % P::COLS;
-        if (r >= rows || n >= cols)
-            continue;
-        float sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < KW; ++w)
-            sum += sums[(w * 16 * FM + r) * P::SUM_LD + n];
-        store_c(g, 0, m0 + r, n0 + n, epilogue_value(g, 0, m0 + r, n0 + n, sum));
-    }
-}
-
-template <int T, bool S32, bool ZEROS, int SPG, int FM, int FN, int NW, int KW, int TS>
-hipError_t launch(const QweightArgs &a, uint32_t programs, hipStream_t s)
-{
-    hipLaunchKernelGGL((qweight_stream_kernel<T, S32, ZEROS, SPG, FM, FN, NW, KW, TS>),
-                       dim3(programs), dim3(64 * NW * KW), (QPanel<SPG, FM, FN, NW, KW, TS>::BYTES),
-                       s, a, fastdiv_make((uint32_t)(a.group_size < a.K ? a.group_size : a.K)));
-    return hipGetLastError();
-}
-
-template <bool S32, bool ZEROS, int SPG, int... SHAPE>
-hipError_t launch_typed(const QweightArgs &a, uint32_t programs, hipStream_t s)
-{
-    return a.a_type == DT_F16 ? launch<DT_F16, S32, ZEROS, SPG, SHAPE...>(a, programs, s)
-                              : launch<DT_BF16, S32, ZEROS, SPG, SHAPE...>(a, programs, s);
-}
-
-template <int SPG, int... SHAPE>
-hipError_t launch_scaled(const QweightArgs &a, uint32_t programs, hipStream_t s)
-{
-    if (a.scale_type == DT_F32)
-        return a.zeros ? launch_typed<true, true, SPG, SHAPE...>(a, programs, s)
-                       : launch_typed<true, false, SPG, SHAPE...>(a, programs, s);
-    return a.zeros ? launch_typed<false, true, SPG, SHAPE...>(a, programs, s)
-                   : launch_typed<false, false, SPG, SHAPE...>(a, programs, s);
-}
-
-// SHAPE: FM, FN, NW, KW, TS
-template <int... SHAPE>
-hipError_t launch_shape(const QweightArgs &a, uint32_t programs, hipStream_t s)
-{
-    if (a.group_size % 128 == 0)
-        return launch_scaled<4, SHAPE...>(a, programs, s);
-    if (a.group_size % 64 == 0)
-        return launch_scaled<2, SHAPE...>(a, programs, s);
-    return launch_scaled<1, SHAPE...>(a, programs, s);
-}
-
-} // namespace
-
-hipError_t launch_qweight_stream(int32_t variant, const QweightArgs &a, uint32_t programs,
-                                 hipStream_t s)
+hipError_t launch_qweight_rows(int32_t variant, const QweightArgs &a, uint32_t programs,
+                               hipStream_t s)
 {
     switch (variant) {
-    case 0: return launch_shape<1, 1, 1, 8, 2>(a, programs, s);
-    case 1: return launch_shape<1, 1, 2, 4, 2>(a, programs, s);
-    case 2: return launch_shape<1, 1, 4, 2, 2>(a, programs, s);
-    case 3: return launch_shape<2, 1, 2, 4, 2>(a, programs, s);
-    case 4: return launch_shape<2, 1, 4, 2, 2>(a, programs, s);
+    case 0: return launch_shape<1, 1, 1, 8, 4, 4>(a, programs, s);
+    case 1: return launch_shape<1, 1, 1, 8, 2, 16>(a, programs, s);
+    case 2: return launch_shape<1, 1, 2, 4, 2, 16>(a, programs, s);
+    case 3: return launch_shape<1, 1, 4, 2, 2, 16>(a, programs, s);
+    case 4: return launch_shape<2, 1, 2, 4, 2, 32>(a, programs, s);
+    case 5: return launch_shape<2, 1, 4, 2, 2, 32>(a, programs, s);
     default: return hipErrorInvalidValue;
     }
 }

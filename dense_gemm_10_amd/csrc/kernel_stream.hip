@@ -1,5 +1,5 @@
-// Grouped products with few rows per group (stream.hpp): 16-bit weights in
-// either order.
+// Grouped products with few rows per group (stream.hpp): 16-bit or fp32
+// weights in either order.
 //
 // K-contiguous B[e] (BT false): lane l's operand of a 16 x 16 x 32 MFMA is
 // 16 bytes of column l mod 16, k = 8 (l / 16) .. + 7: one load each.
@@ -8,13 +8,16 @@
 // registers, two k of one column per register: FN operands, operand j
 // holding columns FN c + j.  Either way a step is 64 k: 128 bytes of a
 // column, or FN * 32 bytes of each row.
+//
+// fp32 has the same pieces of half as many k: lane 16 g + c holds k = 4 g ..
+// 4 g + 3 of 16, and element t of every lane's piece makes MFMA t (16 x 16 x
+// 4), whose four k are 4 g + t.
 #include "stream.hpp"
 
 namespace dg {
 
 namespace {
 
-constexpr int SK = 64;             // k of one step of a wavefront
 
 // 16-bit halves of two words: (lo(a), lo(b)) and (hi(a), hi(b)).
 __device__ __forceinline__ uint32_t pair_lo(uint32_t a, uint32_t b)
@@ -26,22 +29,45 @@ __device__ __forceinline__ uint32_t pair_hi(uint32_t a, uint32_t b)
     return __builtin_amdgcn_perm(b, a, 0x07060302u);
 }
 
-// FN consecutive 16-bit elements, FN = 2, 4 or 8, as words.
-template <int FN> struct Run { uint32_t w[FN / 2]; };
+// FN consecutive elements of ES bytes as words.
+template <int FN, int ES> struct Run { uint32_t w[FN * ES / 4]; };
 
-template <int FN>
-__device__ __forceinline__ Run<FN> load_run(const uint16_t *p)
+template <int FN, int ES>
+__device__ __forceinline__ Run<FN, ES> load_run(const char *p)
 {
-    Run<FN> r;
-    __builtin_memcpy(&r, __builtin_assume_aligned(p, 2 * FN), 2 * FN);
+    Run<FN, ES> r;
+    __builtin_memcpy(&r, __builtin_assume_aligned(p, ES * FN), ES * FN);
     return r;
+}
+
+__device__ __forceinline__ uint32_t word(uint4 v, int i)
+{
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// acc += one piece of A against one piece of B.
+template <int T>
+__device__ __forceinline__ f32x4_t mfma_piece(uint4 a, uint4 b, f32x4_t acc)
+{
+    if constexpr (T == DT_F32) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(word(a, t)),
+                                                       __uint_as_float(word(b, t)), acc, 0, 0, 0);
+        return acc;
+    } else {
+        using frag_t = typename frag_of<T>::type;
+        return mfma_16x16x32(__builtin_bit_cast(frag_t, a), __builtin_bit_cast(frag_t, b), acc);
+    }
 }
 
 template <int T, bool BT, int FM, int FN, int KW>
 __global__ __launch_bounds__(64 * KW) void grouped_stream_kernel(GroupedArgs a)
 {
-    using frag_t = typename frag_of<T>::type;
-    static_assert(!BT || FN == 2 || FN == 4 || FN == 8, "runs of whole words");
+    constexpr int ES = T == DT_F32 ? 4 : 2;      // bytes of an element
+    constexpr int VK = 16 / ES;                  // k of a 16-byte piece
+    constexpr int HK = 4 * VK, SK = 2 * HK;      // k of half a step, and of a step
+    static_assert(!BT || FN == 2 || FN == 4, "runs of 4 to 16 bytes");
     extern __shared__ uint4 lds[];
     const GroupTile t =
         find_group_tile<16 * FM, 16>(a.offsets, a.groups, a.rows, a.tiles_n, blockIdx.x);
@@ -54,73 +80,78 @@ __global__ __launch_bounds__(64 * KW) void grouped_stream_kernel(GroupedArgs a)
     const int rows = (int)(g.M - m0 < 16 * FM ? g.M - m0 : 16 * FM);
     const int cols = (int)(g.N - n0 < 16 * FN ? g.N - n0 : 16 * FN);
 
-    // this lane's sources at k = 0 of its part of a step
-    const uint16_t *ap[FM], *bp[BT ? 1 : FN];
+    // this lane's sources at k = 0 (rows of A, columns of a K-contiguous B),
+    // and at its first k of a step (rows of an N-contiguous B)
+    const char *ap[FM], *bp[BT ? 1 : FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const int r = 16 * i + c < rows ? 16 * i + c : rows - 1;
-        ap[i] = (const uint16_t *)g.A + (m0 + r) * g.lda + 8 * kg;
+        ap[i] = (const char *)g.A + (m0 + r) * g.lda * ES;
     }
     if constexpr (BT) {
         // the last run that starts inside the row; where N cuts it, it
         // reaches into the row's padding, or past the matrix on the last
         // row, which the masked step below therefore takes
         const int run = FN * c < cols ? FN * c : (cols - 1) / FN * FN;
-        bp[0] = (const uint16_t *)g.B + 8 * kg * g.ldb + n0 + run;
+        bp[0] = (const char *)g.B + (VK * kg * g.ldb + n0 + run) * ES;
     } else {
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
             const int n = 16 * j + c < cols ? 16 * j + c : cols - 1;
-            bp[j] = (const uint16_t *)g.B + (n0 + n) * g.ldb + 8 * kg;
+            bp[j] = (const char *)g.B + (n0 + n) * g.ldb * ES;
         }
     }
 
     struct Step {
         uint4 a[2][FM];
         uint4 b[BT ? 1 : 2][BT ? 1 : FN];
-        Run<BT ? FN : 2> run[BT ? 2 : 1][8];
+        Run<BT ? FN : 2, ES> run[BT ? 2 : 1][VK];
     };
     auto load = [&](Step &s, int64_t k) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+            const int64_t kl = k + HK * h + VK * kg;     // this lane's first k
             if constexpr (BT) {
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    s.run[h][r] = load_run<FN>(bp[0] + (k + 32 * h + r) * g.ldb);
+                for (int r = 0; r < VK; ++r)
+                    s.run[h][r] = load_run<FN, ES>(bp[0] + (k + HK * h + r) * g.ldb * ES);
             } else {
 #pragma unroll
                 for (int j = 0; j < FN; ++j)
-                    s.b[h][j] = *(const uint4 *)(bp[j] + k + 32 * h);
+                    s.b[h][j] = *(const uint4 *)(bp[j] + kl * ES);
             }
 #pragma unroll
             for (int i = 0; i < FM; ++i)
-                s.a[h][i] = *(const uint4 *)(ap[i] + k + 32 * h);
+                s.a[h][i] = *(const uint4 *)(ap[i] + kl * ES);
         }
     };
     // the step at k with k >= K read as zero (and no load past a row's end)
     auto load_masked = [&](Step &s, int64_t k) {
         for (int h = 0; h < 2; ++h) {
-            const int64_t kl = k + 32 * h + 8 * kg;      // this lane's first k
+            const int64_t kl = k + HK * h + VK * kg;
 #pragma unroll
             for (int i = 0; i < FM; ++i)
-                s.a[h][i] = load_chunk_tail(ap[i] - 8 * kg, kl, g.K);
+                s.a[h][i] = piece16<T, VK>(ap[i], kl, 1, g.K, true);
             if constexpr (BT) {
 #pragma unroll
-                for (int r = 0; r < 8; ++r) {
-                    uint32_t w[FN / 2] = {};
+                for (int r = 0; r < VK; ++r) {
+                    uint32_t w[FN * ES / 4] = {};
+                    const char *p = (const char *)g.B + ((kl + r) * g.ldb + n0 + FN * c) * ES;
 #pragma unroll
                     for (int e = 0; e < FN; ++e) {
-                        // column FN c + e, if it exists
-                        const uint16_t *p = (const uint16_t *)g.B + (kl + r) * g.ldb + n0;
-                        if (kl + r < g.K && FN * c + e < cols)
-                            w[e / 2] |= (uint32_t)p[FN * c + e] << (16 * (e % 2));
+                        if (kl + r < g.K && FN * c + e < cols) {
+                            if (ES == 4)
+                                w[e] = ((const uint32_t *)p)[e];
+                            else
+                                w[e / 2] |= (uint32_t)((const uint16_t *)p)[e] << (16 * (e % 2));
+                        }
                     }
                     __builtin_memcpy(&s.run[h][r], w, sizeof w);
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < FN; ++j)
-                    s.b[h][j] = load_chunk_tail(bp[j] - 8 * kg, kl, g.K);
+                    s.b[h][j] = piece16<T, VK>(bp[j], kl, 1, g.K, true);
             }
         }
     };
@@ -141,8 +172,13 @@ __global__ __launch_bounds__(64 * KW) void grouped_stream_kernel(GroupedArgs a)
                     uint32_t w[4];
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
-                        const uint32_t x = s.run[h][2 * p].w[j / 2], y = s.run[h][2 * p + 1].w[j / 2];
-                        w[p] = j % 2 ? pair_hi(x, y) : pair_lo(x, y);
+                        if constexpr (ES == 4) {
+                            w[p] = s.run[h][p].w[j];
+                        } else {
+                            const uint32_t x = s.run[h][2 * p].w[j / 2];
+                            const uint32_t y = s.run[h][2 * p + 1].w[j / 2];
+                            w[p] = j % 2 ? pair_hi(x, y) : pair_lo(x, y);
+                        }
                     }
                     b = make_uint4(w[0], w[1], w[2], w[3]);
                 } else {
@@ -150,8 +186,7 @@ __global__ __launch_bounds__(64 * KW) void grouped_stream_kernel(GroupedArgs a)
                 }
 #pragma unroll
                 for (int i = 0; i < FM; ++i)
-                    acc[i][j] = mfma_16x16x32(__builtin_bit_cast(frag_t, s.a[h][i]),
-                                              __builtin_bit_cast(frag_t, b), acc[i][j]);
+                    acc[i][j] = mfma_piece<T>(s.a[h][i], b, acc[i][j]);
             }
     };
 
@@ -193,9 +228,13 @@ hipError_t launch(const GroupedArgs &a, uint32_t programs, hipStream_t s)
     return hipGetLastError();
 }
 
+// 16-bit operands on <FM, FN, KW>, fp32 ones on 8 wavefronts: an fp32 MFMA
+// is eight times slower, so its K is split further.
 template <int FM, int FN, int KW>
 hipError_t launch_typed(const GroupedArgs &a, uint32_t programs, hipStream_t s)
 {
+    if (a.g.ab_type == DT_F32)
+        return launch<DT_F32, FM, FN, 8>(a, programs, s);
     return a.g.ab_type == DT_F16 ? launch<DT_F16, FM, FN, KW>(a, programs, s)
                                  : launch<DT_BF16, FM, FN, KW>(a, programs, s);
 }

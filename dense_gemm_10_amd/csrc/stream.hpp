@@ -1,6 +1,6 @@
 // Products of few rows of A with a large B: each weight is used once or a
 // few times, so the kernels are bound by reading B from memory.  Shared by
-// the grouped products of 16-bit weights (kernel_stream16.hip) and the
+// the grouped products (kernel_stream.hip) and the
 // products with 4-bit weights (kernel_qstream.hip).
 //
 // A workgroup owns 16 FM rows x 16 FN columns of one group's output and its
