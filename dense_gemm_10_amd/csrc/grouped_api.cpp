@@ -319,15 +319,15 @@ hipError_t qrows(const QweightArgs &a, uint32_t p, hipStream_t s)
 }
 const QweightKernel kQGeneric = {"generic", kGroupedGenericTile, kGroupedGenericTile,
                                  launch_qweight_generic};
-const QweightKernel kQ4x16 = {"qstream_4x16", 16, 16, qrows<0>};   // at most 4 rows
-const QweightKernel kQ16x16 = {"qstream_16x16", 16, 16, qrows<1>};
-const QweightKernel kQ16x32 = {"qstream_16x32", 16, 32, qrows<2>};
-const QweightKernel kQ16x64 = {"qstream_16x64", 16, 64, qrows<3>};
-const QweightKernel kQ32x32 = {"qstream_32x32", 32, 32, qrows<4>};
-const QweightKernel kQ32x64 = {"qstream_32x64", 32, 64, qrows<5>};
+const QweightKernel kQ16x16 = {"qstream_16x16", 16, 16, qrows<0>};
+const QweightKernel kQ16x32 = {"qstream_16x32", 16, 32, qrows<1>};
+const QweightKernel kQ16x64 = {"qstream_16x64", 16, 64, qrows<2>};
+const QweightKernel kQ32x32 = {"qstream_32x32", 32, 32, qrows<3>};
+const QweightKernel kQ32x64 = {"qstream_32x64", 32, 64, qrows<4>};
+const QweightKernel kQ32x128 = {"qstream_32x128", 32, 128, qrows<5>};
 const QweightKernel kQ64x256 = {"qtile_64x256", 64, 256, launch_qweight_tile};
-const QweightKernel *const kQweight[] = {&kQ64x256, &kQ32x64, &kQ32x32, &kQ16x64,
-                                         &kQ16x32,  &kQ16x16};
+const QweightKernel *const kQweight[] = {&kQ64x256, &kQ32x128, &kQ32x64, &kQ32x32,
+                                         &kQ16x64,  &kQ16x32,  &kQ16x16};
 
 struct QweightPlan {
     const QweightKernel *kernel;
@@ -335,12 +335,13 @@ struct QweightPlan {
 };
 
 // The matrix-core kernels read A and Q in whole 16-byte pieces and K in
-// whole steps of 32.
+// whole steps of 32, and address a tile (up to 64 rows, 256 columns) with
+// 32-bit byte offsets.
 bool qstream_ok(const dg_qweight_desc *d, bool offsets, const void *A, const void *Q)
 {
     return aligned_to(A, 16) && aligned_to(Q, 16) && d->lda % 8 == 0 && d->ldq % 16 == 0 &&
-           (!offsets || d->stride_q % 16 == 0) && d->K % 32 == 0 && d->K < INT32_MAX - 65536 &&
-           d->lda < (1 << 24) && d->ldq < (1 << 24) && d->lds < (1 << 22);
+           (!offsets || d->stride_q % 16 == 0) && d->K % 32 == 0 && d->lda < (1 << 24) &&
+           d->ldq < (1 << 23) && d->lds < (1 << 21);
 }
 
 int64_t row_tiles(const dg_qweight_desc *d, bool offsets, const QweightKernel &k)
@@ -349,8 +350,8 @@ int64_t row_tiles(const dg_qweight_desc *d, bool offsets, const QweightKernel &k
 }
 
 // From 512 rows a group, if 64 x 256 tiles fill the chip, the tile (us, 4096
-// x 4096, bf16, group size 128): 1024 rows 55 against 94, 2048 rows 115
-// against 187; below, it does not (256 rows: 54 against 25).
+// x 4096, bf16, group size 128): 1024 rows 58 against 67, 2048 rows 115
+// against 130; below, it does not (256 rows: 54 against 24).
 // Else 32 rows where a group has more than 16, and the widest workgroup
 // (each reads A once) that still makes 512 of them for up to 4 rows, 256
 // for more, where A's traffic counts:
@@ -358,13 +359,12 @@ int64_t row_tiles(const dg_qweight_desc *d, bool offsets, const QweightKernel &k
 //            16384 x 4096: 12.5, 10.2, 11.8;  8192 x 8192: 10.5, 12.6, 19.1
 //   16 rows, 4096 x 4096: 7.2, 9.2, 11.8;  16384 x 4096: 18.6, 14.0, 13.3
 //   64 rows, 16384 x 4096: 31.8 on 16 x 64, 31.6 on 32 x 32, 26.9 on 32 x 64
-// 16 columns of up to 4 rows take panels of twice the K, in which most K
-// are one panel.
+//   512 rows, 4096 x 4096: 60.5 on 32 x 32, 44.9 on 32 x 64, 35.5 on 32 x
+//     128 (two column blocks per wavefront halve its reads of A from LDS)
 const QweightKernel *choose(const dg_qweight_desc *d, bool offsets, const void *A, const void *Q)
 {
     if (!qstream_ok(d, offsets, A, Q))
         return &kQGeneric;
-    const bool few = !offsets && d->M <= 4;
     if (const QweightKernel *k = forced_kernel(kQweight))
         return k;
     const int64_t rows = offsets ? d->M / d->groups : d->M;
@@ -374,7 +374,7 @@ const QweightKernel *choose(const dg_qweight_desc *d, bool offsets, const void *
         if (rows_fit && ceil_div(d->N, k->bn) >= ceil_div(want, row_tiles(d, offsets, *k)))
             return k;
     }
-    return few ? &kQ4x16 : &kQ16x16;
+    return &kQ16x16;
 }
 
 dg_status make_plan(const dg_qweight_desc *d, bool offsets, const void *A, const void *Q,

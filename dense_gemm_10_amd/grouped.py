@@ -8,6 +8,7 @@ Nothing is copied, cast or allocated, apart from C when none is given.
 from __future__ import annotations
 
 import ctypes
+import sys
 
 from . import (DG_BF16, DG_COL_MAJOR, DG_F16, DG_F32, DG_ROW_MAJOR, DG_SUCCESS, DgError, _ACT,
                _DTYPE, _ORDER, _enum, _load)
@@ -137,7 +138,7 @@ def _code(t):
     """dg_dtype of a tensor."""
     global _types
     if _types is None:
-        import torch
+        torch = sys.modules["torch"]       # a tensor was passed: it is imported
         _types = {torch.float32: DG_F32, torch.bfloat16: DG_BF16, torch.float16: DG_F16}
     code = _types.get(t.dtype)
     if code is None:
@@ -161,8 +162,7 @@ def _same_device(device, **others):
 
 
 def _check_offsets(offsets, groups):
-    import torch
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() != groups + 1 or \
+    if offsets.dtype != sys.modules["torch"].int32 or offsets.dim() != 1 or offsets.numel() != groups + 1 or \
             not offsets.is_contiguous():
         raise ValueError(f"offsets: a contiguous int32 tensor of {groups + 1} entries is wanted")
 
@@ -171,8 +171,7 @@ def _output(C, shape, dtype, A, beta):
     if C is None:
         if beta != 0.0:
             raise ValueError("beta != 0 needs an input C")
-        import torch
-        return torch.empty(shape, dtype=dtype or A.dtype, device=A.device)
+        return sys.modules["torch"].empty(shape, dtype=dtype or A.dtype, device=A.device)
     if C.shape != shape:
         raise ValueError(f"C: shape {tuple(C.shape)}, {shape} is wanted")
     if dtype is not None and C.dtype != dtype:
@@ -193,12 +192,15 @@ def _bias(bias, groups, N, grouped):
 
 def _launch(entry, name, device, stream, *args):
     """entry(*args, stream) with `device` current, on its current stream by
-    default."""
-    import torch
-    if torch.cuda.current_device() != device:
-        with torch.cuda.device(device):
+    default (the raw handle: building a torch.cuda.Stream takes longer than
+    the launch's argument checks)."""
+    cuda = sys.modules["torch"].cuda
+    if cuda.current_device() != device:
+        with cuda.device(device):
             return _launch(entry, name, device, stream, *args)
-    st = entry(*args, torch.cuda.current_stream(device).cuda_stream if stream is None else stream)
+    if stream is None:
+        stream = sys.modules["torch"]._C._cuda_getCurrentRawStream(device)
+    st = entry(*args, stream)
     if st != DG_SUCCESS:
         raise DgError(st, name)
 
@@ -278,7 +280,7 @@ def gemm_qweight(A, Q, scales, zeros=None, C=None, *, group_size, offsets=None, 
     None for 8.  With offsets (int32, groups + 1, on the GPU), Q, scales,
     zeros and optionally bias have a leading dimension of groups, and each
     row of A uses its group's weights; rows of no group are left alone."""
-    import torch
+    uint8 = sys.modules["torch"].uint8
     ashape, qshape, sshape = A.shape, Q.shape, scales.shape
     grouped = offsets is not None
     dims = 3 if grouped else 2
@@ -287,12 +289,12 @@ def gemm_qweight(A, Q, scales, zeros=None, C=None, *, group_size, offsets=None, 
                          "ceil(K / group_size)) are wanted")
     M, K = ashape
     N, per_row = qshape[-2], -(-K // group_size)
-    if Q.dtype != torch.uint8 or qshape[-1] != (K + 1) // 2:
+    if Q.dtype != uint8 or qshape[-1] != (K + 1) // 2:
         raise ValueError(f"Q: uint8 rows of {(K + 1) // 2} bytes are wanted")
     if sshape[-1] != per_row or sshape[:-1] != qshape[:-1]:
         raise ValueError(f"scales: shape {tuple(sshape)} for {N} rows of {per_row} groups")
     qstride, sstride = Q.stride(), scales.stride()
-    if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != sshape or
+    if zeros is not None and (zeros.dtype != uint8 or zeros.shape != sshape or
                               zeros.stride() != sstride):
         raise ValueError("zeros: uint8 with the shape and strides of scales is wanted")
     groups = stride_q = stride_s = 0

@@ -264,6 +264,44 @@ def test_streams_at_once():
         assert torch.equal(C.cpu().double(), ref * (i // 2 + 1))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_empty_sizes(dtype):
+    """K = 0 gives act(beta C + bias), no rows gives beta C (0) weight
+    gradients, no groups or columns change nothing."""
+    dt = DT[dtype]
+
+    def t(*shape):
+        return torch.ones(shape, dtype=dt, device="cuda")
+
+    off = _offsets([1, 3, 4])
+    bias = torch.tensor([[1.0, 2.0, 3.0], [4.0, 5.0, 6.0]], dtype=dt, device="cuda")
+    C = torch.full((5, 3), 7.0, dtype=dt, device="cuda")
+    dg.gemm_grouped(t(5, 0), t(2, 0, 3), off, C, beta=2.0, bias=bias)
+    want = [[7.0] * 3, [15.0, 16.0, 17.0], [15.0, 16.0, 17.0], [18.0, 19.0, 20.0], [7.0] * 3]
+    assert C.tolist() == want
+    D = torch.full((2, 4, 3), 2.0, dtype=dt, device="cuda")
+    dg.gemm_grouped_k(t(0, 4).t(), t(0, 3), _offsets([0, 0, 0]), D, beta=1.5)
+    assert bool((D == 3.0).all())
+    assert bool((dg.gemm_grouped_k(t(0, 4).t(), t(0, 3), _offsets([0, 0, 0])) == 0.0).all())
+    before = C.clone()
+    dg.gemm_grouped(t(5, 2), t(0, 2, 3), _offsets([0]), C)
+    assert torch.equal(C, before)
+    assert dg.gemm_grouped(t(5, 2), t(2, 2, 0), off).shape == (5, 0)
+    assert dg.gemm_grouped_k(t(5, 0).t(), t(5, 3), off).shape == (2, 0, 3)
+    assert dg.gemm_grouped(t(0, 2), t(2, 2, 3), _offsets([0, 0, 0])).shape == (0, 3)
+
+
+def test_one_group_longer_than_the_mean():
+    """Many groups, one of which has nearly every row, on each kernel that
+    the mean length chooses."""
+    gen = torch.Generator().manual_seed(21)
+    for groups, rows, K, N in ((40, 200, 96, 72), (30, 400, 64, 136), (12, 600, 72, 264), (9, 2400, 64, 136)):
+        A, B = ints(gen, rows, K, dtype=torch.bfloat16), ints(gen, groups, K, N, dtype=torch.bfloat16)
+        off = [0] * 3 + [2] + [rows - 1] * (groups - 4) + [rows]
+        got = dg.gemm_grouped(A.cuda(), B.cuda(), _offsets(off), out_dtype=torch.float32)
+        assert torch.equal(got.cpu().double(), _ref_m(A, B, off, torch.float32)[0]), groups
+
+
 def test_runs_repeat_bit_for_bit():
     gen = torch.Generator().manual_seed(6)
     groups, rows, K, N = 6, 500, 264, 264

@@ -138,6 +138,56 @@ def test_qweight_pointers():
     assert _qrun(d) == bad
 
 
+# ---- the kernel a problem gets ------------------------------------------------------
+def _kernel(text):
+    return dict(t.split("=") for t in text.split())["kernel"]
+
+
+@pytest.mark.parametrize("kw,kernel", [
+    (dict(groups=8, rows=8, K=1024, N=1024), "stream_16x32"),
+    (dict(groups=64, rows=64, K=2048, N=1024), "stream_16x64"),
+    (dict(groups=64, rows=1024, K=2048, N=2048), "stream_32x64"),
+    (dict(groups=20, rows=1000, K=1024, N=4096), "mfma16_128x128"),
+    (dict(groups=7, rows=4095, K=1000, N=4097, b_order="col"), "mfma16_128x128x64"),
+    (dict(groups=16, rows=8192, K=4096, N=4096), "mfma16_256x256"),
+    (dict(groups=5, rows=1000, K=512, N=260, a_type="f32"), "stream_32x64"),
+    (dict(groups=16, rows=8192, K=2048, N=4096, a_type="f32"), "mfma_f32_128x128"),
+    (dict(groups=4, rows=100, K=33, N=64), "generic"),              # lda off the 16-byte grid
+    (dict(groups=4, rows=100, K=64, N=33), "generic"),              # ldb
+    (dict(groups=4, rows=100, K=64, N=33, b_order="col"), "mfma16_128x128"),
+    (dict(groups=4, rows=100, K=64, N=64, stride_b=4100), "generic"),
+    (dict(groups=1, rows=100, K=64, N=64, stride_b=4100), "mfma16_128x128"),
+    (dict(ragged="k", groups=16, rows=8192, M=2048, N=2048), "mfma16_128x128"),
+    (dict(ragged="k", groups=8, rows=8192, M=1024, N=2048), "mfma16_256x256"),
+    (dict(ragged="k", groups=8, rows=8192, M=1024, N=2048, a_type="f32"), "mfma_f32_128x128"),
+    (dict(ragged="k", groups=8, rows=8192, M=1001, N=2048), "generic"),
+], ids=str)
+def test_kernel_of_a_grouped_problem(kw, kernel, monkeypatch):
+    monkeypatch.delenv("DG_FORCE_GROUPED", raising=False)
+    kw = dict({"ragged": "m"}, **kw)
+    assert _kernel(dg.dg_gemm_grouped_describe(dg.make_grouped_desc(**kw))) == kernel
+    # a forced kernel never replaces the generic one, whose operands no other takes
+    monkeypatch.setenv("DG_FORCE_GROUPED", "mfma16_256x256")
+    forced = _kernel(dg.dg_gemm_grouped_describe(dg.make_grouped_desc(**kw)))
+    assert forced == ("generic" if kernel == "generic" else kernel if kw.get("a_type") == "f32"
+                      else "mfma16_256x256")
+
+
+@pytest.mark.parametrize("M,N,K,g,kw,kernel", [
+    (1, 4096, 4096, 128, {}, "qstream_16x16"), (1, 16384, 8192, 64, {}, "qstream_16x32"),
+    (16, 16384, 4096, 128, {}, "qstream_16x64"), (64, 4096, 4096, 128, {}, "qstream_32x32"),
+    (128, 4096, 4096, 128, {}, "qstream_32x64"), (512, 4096, 4096, 128, {}, "qstream_32x128"),
+    (2048, 4096, 4096, 128, {}, "qtile_64x256"), (5, 64, 4112, 128, {}, "generic"),
+    (5, 64, 128, 32, dict(ldq=72), "generic"), (5, 64, 128, 32, dict(lda=132), "generic"),
+    (64, 2048, 2048, 128, dict(groups=64), "qstream_16x64"),
+    (64, 2048, 2048, 128, dict(groups=64, stride_q=2048 * 1024 + 8), "generic"),
+    (1, 64, 2 ** 20, 32, dict(ldq=2 ** 23), "generic"),
+], ids=str)
+def test_kernel_of_a_4_bit_problem(M, N, K, g, kw, kernel, monkeypatch):
+    monkeypatch.delenv("DG_FORCE_GROUPED", raising=False)
+    assert _kernel(dg.dg_gemm_qweight_describe(dg.make_qweight_desc(M, N, K, g, **kw))) == kernel
+
+
 # ---- the torch entry points refuse before any GPU call ---------------------------
 def _t(*shape, dtype=torch.bfloat16):
     return torch.zeros(shape, dtype=dtype)

@@ -179,6 +179,44 @@ def test_nan_rows_and_scales_stay_where_they_are(M):
     assert not bool(got[1].isfinite().any()) and not bool(got[0, 7].isfinite())
 
 
+def test_empty_sizes():
+    def z(*shape, dtype=torch.bfloat16):
+        return torch.zeros(shape, dtype=dtype, device="cuda")
+
+    C = torch.full((2, 3), 4.0, device="cuda")
+    dg.gemm_qweight(z(2, 0), z(3, 0, dtype=torch.uint8), z(3, 0), None, C, group_size=32, beta=0.5,
+                    bias=torch.tensor([1.0, 2.0, 3.0], device="cuda"))
+    assert C.tolist() == [[3.0, 4.0, 5.0]] * 2
+    assert dg.gemm_qweight(z(0, 64), z(3, 32, dtype=torch.uint8), z(3, 2), group_size=32).shape == (0, 3)
+    assert dg.gemm_qweight(z(2, 64), z(0, 32, dtype=torch.uint8), z(0, 2), group_size=32).shape == (2, 0)
+    dg.gemm_qweight(z(2, 64), z(0, 3, 32, dtype=torch.uint8), z(0, 3, 2), None, C, group_size=32,
+                    offsets=_offsets([0]))
+    assert C.tolist() == [[3.0, 4.0, 5.0]] * 2
+
+
+def test_runs_repeat_bit_for_bit():
+    gen = torch.Generator().manual_seed(6)
+    for M, N, K, g in ((1, 264, 4352, 128), (40, 520, 1024, 32), (700, 264, 512, 64)):
+        q, scales, zeros = _make(gen, (), N, K, g, torch.bfloat16, True, False)
+        A = torch.randn(M, K, generator=gen).bfloat16().cuda()
+        args = A, _pack(q).cuda(), scales.cuda(), zeros.cuda()
+        first = dg.gemm_qweight(*args, group_size=g)
+        for _ in range(5):
+            assert torch.equal(dg.gemm_qweight(*args, group_size=g), first)
+
+
+@pytest.mark.parametrize("size", [(600, 2000, 288, 96), (1024, 1040, 512, 128), (2050, 264, 160, 32)], ids=str)
+def test_many_rows(size):
+    """Sizes that the 64 x 256 tile takes, and its edges."""
+    M, N, K, g = size
+    gen = torch.Generator().manual_seed(M)
+    q, scales, zeros = _make(gen, (), N, K, g, torch.float16, True, True)
+    A = ints(gen, M, K, dtype=torch.float16)
+    got = dg.gemm_qweight(A.cuda(), _pack(q).cuda(), scales.cuda(), zeros.cuda(), group_size=g,
+                          out_dtype=torch.float32)
+    assert torch.equal(got.cpu().double(), A.double() @ _weights(q, scales, zeros, g).t())
+
+
 def test_weights_past_2_31_bytes():
     gen = torch.Generator(device="cuda").manual_seed(1)
     N, K, g, groups = 4096, 8192, 128, 130                       # 2.18e9 bytes of Q
