@@ -49,9 +49,9 @@ SOURCES = [
     "kernel_sliver.hip",
     "grouped_api.cpp",
     "kernel_grouped_generic.hip",
-    "kernel_grouped16_m256.hip",
+    "kernel_grouped16_m256_bf16.hip",
+    "kernel_grouped16_m256_f16.hip",
     "kernel_grouped16_m128.hip",
-    "kernel_grouped16_m128x64.hip",
     "kernel_grouped16_k256.hip",
     "kernel_grouped16_k128.hip",
     "kernel_grouped_f32.hip",

@@ -205,8 +205,8 @@ struct QweightArgs {
 hipError_t launch_grouped_generic(const GroupedArgs &a, bool ragged_k, uint32_t programs,
                                   hipStream_t s);
 // 16-bit matrix-core tiles (256 x 256 and 128 x 128)
-hipError_t launch_grouped16_m256(const GroupedArgs &a, uint32_t programs, hipStream_t s);
-hipError_t launch_grouped16_m128x64(const GroupedArgs &a, uint32_t programs, hipStream_t s);
+hipError_t launch_grouped16_m256_bf16(const GroupedArgs &a, uint32_t programs, hipStream_t s);
+hipError_t launch_grouped16_m256_f16(const GroupedArgs &a, uint32_t programs, hipStream_t s);
 hipError_t launch_grouped16_m128(const GroupedArgs &a, uint32_t programs, hipStream_t s);
 hipError_t launch_grouped16_k256(const GroupedArgs &a, uint32_t programs, hipStream_t s);
 hipError_t launch_grouped16_k128(const GroupedArgs &a, uint32_t programs, hipStream_t s);

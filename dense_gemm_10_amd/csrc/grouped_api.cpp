@@ -3,7 +3,6 @@
 // launch.  Nothing is known of the groups' lengths here: the grid covers an
 // upper bound of the tiles, and the choice goes by the mean length.
 #include <hip/hip_runtime.h>
-#include <math.h>
 #include <stdint.h>
 #include <stdio.h>
 #include <stdlib.h>
@@ -144,20 +143,25 @@ hipError_t stream_m(const GroupedArgs &a, uint32_t p, hipStream_t s)
     return launch_grouped_stream(V, a, p, s);
 }
 
+hipError_t tile256_m(const GroupedArgs &a, uint32_t p, hipStream_t s)
+{
+    return a.g.ab_type == DT_F16 ? launch_grouped16_m256_f16(a, p, s)
+                                 : launch_grouped16_m256_bf16(a, p, s);
+}
+
 const GroupedKernel kGeneric = {"generic", kGroupedGenericTile, kGroupedGenericTile, generic_m,
                                 generic_k};
-const GroupedKernel kTile256 = {"mfma16_256x256", 256, 256, launch_grouped16_m256,
+const GroupedKernel kTile256 = {"mfma16_256x256", 256, 256, tile256_m,
                                 launch_grouped16_k256};
 const GroupedKernel kTile128 = {"mfma16_128x128", 128, 128, launch_grouped16_m128,
                                 launch_grouped16_k128};
-const GroupedKernel kTile128x64 = {"mfma16_128x128x64", 128, 128, launch_grouped16_m128x64, nullptr};
 const GroupedKernel kTileF32 = {"mfma_f32_128x128", 128, 128, launch_grouped_f32_m,
                                 launch_grouped_f32_k};
 const GroupedKernel kStream16x32 = {"stream_16x32", 16, 32, stream_m<0>, nullptr};
 const GroupedKernel kStream16x64 = {"stream_16x64", 16, 64, stream_m<1>, nullptr};
 const GroupedKernel kStream32x64 = {"stream_32x64", 32, 64, stream_m<2>, nullptr};
-const GroupedKernel *const kGrouped16[] = {&kTile256,     &kTile128,     &kTile128x64,
-                                           &kStream16x32, &kStream16x64, &kStream32x64};
+const GroupedKernel *const kGrouped16[] = {&kTile256, &kTile128, &kStream16x32, &kStream16x64,
+                                           &kStream32x64};
 const GroupedKernel *const kGroupedF32[] = {&kTileF32, &kStream16x32, &kStream16x64, &kStream32x64};
 
 // The kernel of `table` that DG_FORCE_GROUPED names (benchmarking and
@@ -188,7 +192,7 @@ bool mfma_ok(const dg_grouped_desc *d, const void *A, const void *B)
 }
 
 // The kernel for a problem.  Group lengths are unknown; the mean stands for
-// them, and every group is taken to end inside a tile (0.6 of one lost).
+// them, and half the groups are taken to end in one more tile.
 //
 // Ragged rows, by the mean rows of a group (us, MI355X, bf16):
 //   up to 8 rows, the 16-row streaming kernels: 64 groups, 512 rows, 2048 x
@@ -203,14 +207,12 @@ bool mfma_ok(const dg_grouped_desc *d, const void *A, const void *B)
 //     groups, 512 x 260: 10 against 63; 4096 rows, 16 groups, 2048 x 2048:
 //     332-390 against 393-407) and takes the tile above (8192 rows, 2048 x
 //     4096: 1151-1166 against 1228-1440);
-//   above, 16 bits, a tile.  Below 128 rows the 128 x 128 one with a deep
-//     ring (1000 rows, 20 groups, 1024 x 4096: 36 against 40 on the one with
-//     64-deep stages); else the cheaper of 256 x 256 and 128 x 128 with
-//     64-deep stages, in whole waves of 256 workgroups for the first (one per
-//     CU) and waves of 512, plus half a one for the last, at 0.64 of the cost
-//     for the second, each costing its K and about 450 k of start and
-//     epilogue (8192 rows, 16 groups, 4096 x 4096: 326 against 347; 4095
-//     rows, 7 groups, 1000 x 4097: 78 against 66).
+//   above, 16 bits, a tile: 256 x 256 (with half-height tiles, see
+//     grouped16.hpp) for groups of 128 rows and more, K from 768 and at
+//     least 128 tiles, else 128 x 128 (8192 rows, 16 groups, 4096 x 4096:
+//     305-313 against 390-418; 2000 rows, 16 groups, 4096 x 2048: 78 against
+//     103; but 1000 rows, 4 groups, 4096 x 1024, 28 tiles: 61-73 against
+//     49-51, and 6000 rows, 48 groups, 512 x 1024: 32 against 27).
 // Ragged K: the 128 x 128 tile, whose second workgroup on a CU covers the
 // other's epilogue (16 groups of 2048 x 2048, 8192 rows: 103 against 107;
 // 32 of 512 x 1024: 18-21 against 24), unless the groups are long and 256 x
@@ -226,7 +228,7 @@ const GroupedKernel *choose(const dg_grouped_desc *d, const void *A, const void 
     if (f32 && rk)
         return &kTileF32;
     const double mean = (double)d->rows / (double)d->groups;
-    const double n256 = (double)ceil_div(d->N, 256), n128 = (double)ceil_div(d->N, 128);
+    const double n256 = (double)ceil_div(d->N, 256);
     if (rk) {
         const double tiles = (double)d->groups * (double)ceil_div(d->M, 256) * n256;
         return mean >= 768 && tiles >= 240 ? &kTile256 : &kTile128;
@@ -239,12 +241,8 @@ const GroupedKernel *choose(const dg_grouped_desc *d, const void *A, const void 
     if (f32)
         return row_tiles(d->rows, d->groups, 128) * ceil_div(d->N, 128) < 4 * kCus ? &kStream32x64
                                                                                    : &kTileF32;
-    if (mean < 128)
-        return &kTile128;
-    const double lost = 0.6 * (double)d->groups, k = (double)d->K;
-    const double waves256 = ceil(((double)d->rows / 256 + lost) * n256 / kCus);
-    const double waves128 = ((double)d->rows / 128 + lost) * n128 / (2 * kCus) + 0.5;
-    return waves256 * (k + 490) < 0.64 * waves128 * (k + 400) ? &kTile256 : &kTile128x64;
+    const double tiles = ((double)d->rows / 256 + 0.5 * (double)d->groups) * n256;
+    return mean >= 128 && d->K >= 768 && tiles >= 128 ? &kTile256 : &kTile128;
 }
 
 dg_status make_plan(const dg_grouped_desc *d, const void *A, const void *B, GroupedPlan *p)

@@ -9,9 +9,9 @@ namespace dg {
 
 #define STUB(name) \
     hipError_t name(const GroupedArgs &, uint32_t, hipStream_t) { return hipErrorInvalidValue; }
-STUB(launch_grouped16_m256)
+STUB(launch_grouped16_m256_bf16)
+STUB(launch_grouped16_m256_f16)
 STUB(launch_grouped16_m128)
-STUB(launch_grouped16_m128x64)
 STUB(launch_grouped16_k256)
 STUB(launch_grouped16_k128)
 STUB(launch_grouped_f32_m)

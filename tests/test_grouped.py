@@ -302,6 +302,57 @@ def test_one_group_longer_than_the_mean():
         assert torch.equal(got.cpu().double(), _ref_m(A, B, off, torch.float32)[0]), groups
 
 
+@pytest.mark.parametrize("order", ["kn", "nk"])
+@pytest.mark.parametrize("rows,lengths", [
+    (4200, [300, 0, 128, 129, 256, 1, 640, 512, 127, 1000, 255, 257, 300, 295]),   # every kind of last tile
+    (2600, [2600]), (2560, [1280, 1280]), (3000, [1500, 100, 1400]),
+    (5000, [90] * 10 + [100] * 10 + [1500, 1600]),
+])
+def test_whole_and_half_tiles(rows, lengths, order):
+    """The 256 x 256 tile with its half-height tiles: last tiles of up to and
+    over 128 rows, with and without a partly filled last wave to cut."""
+    gen = torch.Generator().manual_seed(rows)
+    groups, K = len(lengths), 64
+    off = [0]
+    for n in lengths:
+        off.append(off[-1] + n)
+    assert off[-1] <= rows
+    A = ints(gen, rows, K, dtype=torch.bfloat16)
+    for N in (264, 1100 if order == "nk" else 1104, 2048):
+        B = ints(gen, groups, K, N, dtype=torch.bfloat16)
+        Bd = B.cuda() if order == "kn" else B.transpose(1, 2).contiguous().cuda().transpose(1, 2)
+        C = torch.full((rows, N), float("nan"), device="cuda")
+        with pytest.MonkeyPatch.context() as m:
+            m.setenv("DG_FORCE_GROUPED", "mfma16_256x256")
+            dg.gemm_grouped(A.cuda(), Bd, _offsets(off), C)
+        ref, _, inside = _ref_m(A, B, off, torch.float32)
+        got = C.cpu().double()
+        assert torch.equal(got[inside], ref[inside]), N
+        assert bool(got[~inside].isnan().all())
+
+
+@pytest.mark.parametrize("kernel", ["mfma16_256x256", "mfma16_128x128", "mfma_f32_128x128", "stream_16x32",
+                                    "stream_16x64", "stream_32x64"])
+def test_every_kernel_takes_every_pattern(kernel, monkeypatch):
+    """The kernel a problem gets depends on its sizes alone; each of them is
+    right for any lengths."""
+    monkeypatch.setenv("DG_FORCE_GROUPED", kernel)
+    dtype = torch.float32 if "f32" in kernel else torch.bfloat16
+    gen = torch.Generator().manual_seed(31)
+    for groups, rows, K, N in ((3, 7, 40, 24), (70, 500, 96, 136), (5, 900, 72, 520)):
+        A, B = ints(gen, rows, K, dtype=dtype), ints(gen, groups, K, N, dtype=dtype)
+        G = ints(gen, rows, N, dtype=dtype)
+        for pattern in ("random", "one", "edges", "none"):
+            off = offsets_like(pattern, groups, rows, gen)
+            C = torch.full((rows, N), 5.0, device="cuda")
+            dg.gemm_grouped(A.cuda(), B.cuda(), _offsets(off), C)
+            ref, _, inside = _ref_m(A, B, off, torch.float32)
+            ref[~inside] = 5.0
+            assert torch.equal(C.cpu().double(), ref), (pattern, off)
+            got = dg.gemm_grouped_k(A.cuda().t(), G.cuda(), _offsets(off), out_dtype=torch.float32)
+            assert torch.equal(got.cpu().double(), _ref_k(A.t(), G, off, torch.float32)[0])
+
+
 def test_runs_repeat_bit_for_bit():
     gen = torch.Generator().manual_seed(6)
     groups, rows, K, N = 6, 500, 264, 264

@@ -148,7 +148,8 @@ def _kernel(text):
     (dict(groups=64, rows=64, K=2048, N=1024), "stream_16x64"),
     (dict(groups=64, rows=1024, K=2048, N=2048), "stream_32x64"),
     (dict(groups=20, rows=1000, K=1024, N=4096), "mfma16_128x128"),
-    (dict(groups=7, rows=4095, K=1000, N=4097, b_order="col"), "mfma16_128x128x64"),
+    (dict(groups=7, rows=4095, K=1000, N=4097, b_order="col"), "mfma16_256x256"),
+    (dict(groups=4, rows=1000, K=4096, N=1024), "mfma16_128x128"),
     (dict(groups=16, rows=8192, K=4096, N=4096), "mfma16_256x256"),
     (dict(groups=5, rows=1000, K=512, N=260, a_type="f32"), "stream_32x64"),
     (dict(groups=16, rows=8192, K=2048, N=4096, a_type="f32"), "mfma_f32_128x128"),

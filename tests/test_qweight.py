@@ -179,6 +179,34 @@ def test_nan_rows_and_scales_stay_where_they_are(M):
     assert not bool(got[1].isfinite().any()) and not bool(got[0, 7].isfinite())
 
 
+@pytest.mark.parametrize("kernel", ["qstream_16x16", "qstream_16x32", "qstream_16x64", "qstream_32x32",
+                                    "qstream_32x64", "qstream_32x128", "qtile_64x256"])
+def test_every_kernel(kernel, monkeypatch):
+    """The kernel depends on the sizes alone; each is right for any rows,
+    columns, K, group size and lengths."""
+    monkeypatch.setenv("DG_FORCE_GROUPED", kernel)
+    gen = torch.Generator().manual_seed(17)
+    for M, N, K, g, dt, with_zeros in ((1, 300, 4384, 128, torch.bfloat16, False), (70, 130, 288, 96, torch.float16, True),
+                                       (33, 16, 64, 64, torch.bfloat16, True), (130, 520, 1056, 32, torch.float16, False)):
+        q, scales, zeros = _make(gen, (), N, K, g, dt, with_zeros, True)
+        A = ints(gen, M, K, dtype=dt)
+        got = dg.gemm_qweight(A.cuda(), _pack(q).cuda(), scales.cuda(), _dev(zeros), group_size=g,
+                              out_dtype=torch.float32)
+        assert torch.equal(got.cpu().double(), A.double() @ _weights(q, scales, zeros, g).t()), (M, N, K)
+    groups, rows, N, K, g = 70, 300, 72, 192, 64
+    q, scales, zeros = _make(gen, (groups,), N, K, g, torch.bfloat16, True, True)
+    A, W = ints(gen, rows, K, dtype=torch.bfloat16), _weights(q, scales, zeros, g)
+    for pattern in ("random", "one", "edges"):
+        off = offsets_like(pattern, groups, rows, gen)
+        C = torch.full((rows, N), 5.0, device="cuda")
+        dg.gemm_qweight(A.cuda(), _pack(q).cuda(), scales.cuda(), zeros.cuda(), C, group_size=g,
+                        offsets=_offsets(off))
+        ref = torch.full((rows, N), 5.0, dtype=torch.float64)
+        for e, (lo, hi) in enumerate(groups_of(off, rows)):
+            ref[lo:hi] = A[lo:hi].double() @ W[e].t()
+        assert torch.equal(C.cpu().double(), ref), pattern
+
+
 def test_empty_sizes():
     def z(*shape, dtype=torch.bfloat16):
         return torch.zeros(shape, dtype=dtype, device="cuda")
