@@ -174,17 +174,21 @@ void qweight_stream_kernel(QweightArgs a, FastDiv by_group)
     using P = QPanel<SPG, FM, FN, NW, KW, TS, MR>;
     extern __shared__ uint4 lds[];
     GroupTile t;
+    constexpr int G = 8;
     if (a.offsets) {
-        t = find_group_tile<16 * FM, 16>(a.offsets, a.groups, a.rows, a.tiles_n, blockIdx.x);
+        t = find_group_tile<16 * FM, G>(a.offsets, a.groups, a.rows, a.tiles_n, blockIdx.x);
         if (t.group < 0)
             return;
     } else {
-        // column tile by column tile, the row tiles of one (which read the
-        // same codes) together, dealt to the XCDs in contiguous runs
+        // the same order without groups: contiguous runs to the XCDs, bands
+        // of G row tiles walked column by column, so that an XCD's running
+        // tiles share codes and rows of A
         const uint32_t tm = ((uint32_t)a.rows + 16 * FM - 1) / (16 * FM);
         const uint32_t N = tm * a.tiles_n, x = blockIdx.x % kNumXcd, r = N % kNumXcd;
         const uint32_t L = x * (N / kNumXcd) + (x < r ? x : r) + blockIdx.x / kNumXcd;
-        t = GroupTile{0, 0, a.rows, L % tm, L / tm};
+        const uint32_t band = L / (G * a.tiles_n), o = L - band * (G * a.tiles_n);
+        const uint32_t left = tm - band * G, h = left < G ? left : G;
+        t = GroupTile{0, 0, a.rows, band * G + o % h, o / h};
     }
     const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, kg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
