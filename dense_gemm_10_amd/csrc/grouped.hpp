@@ -219,6 +219,7 @@ hipError_t launch_grouped_stream(int32_t variant, const GroupedArgs &a, uint32_t
 hipError_t launch_qweight_rows(int32_t variant, const QweightArgs &a, uint32_t programs,
                                hipStream_t s);
 hipError_t launch_qweight_tile(const QweightArgs &a, uint32_t programs, hipStream_t s);
+hipError_t launch_qweight_wide_tile(const QweightArgs &a, uint32_t programs, hipStream_t s);
 hipError_t launch_qweight_generic(const QweightArgs &a, uint32_t programs, hipStream_t s);
 
 constexpr int kGroupedGenericTile = 64;

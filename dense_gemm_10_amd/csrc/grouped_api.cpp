@@ -324,6 +324,8 @@ const QweightKernel kQ32x32 = {"qstream_32x32", 32, 32, qrows<3>};
 const QweightKernel kQ32x64 = {"qstream_32x64", 32, 64, qrows<4>};
 const QweightKernel kQ32x128 = {"qstream_32x128", 32, 128, qrows<5>};
 const QweightKernel kQ64x256 = {"qtile_64x256", 64, 256, launch_qweight_tile};
+// group sizes that are multiples of 128 only; its choice has a rule of its own
+const QweightKernel kQ64x512 = {"qtile_64x512", 64, 512, launch_qweight_wide_tile};
 const QweightKernel *const kQweight[] = {&kQ64x256, &kQ32x128, &kQ32x64, &kQ32x32,
                                          &kQ16x64,  &kQ16x32,  &kQ16x16};
 
@@ -333,7 +335,7 @@ struct QweightPlan {
 };
 
 // The matrix-core kernels read A and Q in whole 16-byte pieces and K in
-// whole steps of 32, and address a tile (up to 64 rows, 256 columns) with
+// whole steps of 32, and address a tile (up to 64 rows, 512 columns) with
 // 32-bit byte offsets.
 bool qstream_ok(const dg_qweight_desc *d, bool offsets, const void *A, const void *Q)
 {
@@ -347,9 +349,22 @@ int64_t row_tiles(const dg_qweight_desc *d, bool offsets, const QweightKernel &k
     return offsets ? row_tiles(d->M, d->groups, k.bm) : ceil_div(d->M, k.bm);
 }
 
+// Times a tile's place on the chip is taken: one workgroup per CU.
+int64_t chip_passes(int64_t row_tiles, int64_t n, int64_t bn)
+{
+    const int64_t per_pass = 256, cols = ceil_div(n, bn);
+    if (row_tiles > INT64_MAX / cols)
+        return INT64_MAX / 8;
+    return ceil_div(row_tiles * cols, per_pass);
+}
+
 // From 512 rows a group, if 64 x 256 tiles fill the chip, the tile (us, 4096
 // x 4096, bf16, group size 128): 1024 rows 58 against 67, 2048 rows 115
-// against 130; below, it does not (256 rows: 54 against 24).
+// against 130; below, it does not (256 rows: 54 against 24).  A pass of 64 x 512
+// tiles over the chip takes 98 us where one of 64 x 256 takes 57 (four
+// column blocks per wavefront read a row of A once, but hold 256 registers),
+// so they are taken where they need less than 4/7 of the passes: 2048 rows
+// 102 against 112, 8192 x 8192 370 against 409; 1024 rows 98 against 57.
 // Else 32 rows where a group has more than 16, and the widest workgroup
 // (each reads A once) that still makes 512 of them for up to 4 rows, 256
 // for more, where A's traffic counts:
@@ -363,14 +378,21 @@ const QweightKernel *choose(const dg_qweight_desc *d, bool offsets, const void *
 {
     if (!qstream_ok(d, offsets, A, Q))
         return &kQGeneric;
+    const bool wide = d->group_size % 128 == 0;
+    const QweightKernel *const wide_only[] = {&kQ64x512};
+    if (const QweightKernel *k = wide ? forced_kernel(wide_only) : nullptr)
+        return k;
     if (const QweightKernel *k = forced_kernel(kQweight))
         return k;
     const int64_t rows = offsets ? d->M / d->groups : d->M;
     const int64_t want = rows <= 4 ? 512 : 256;
     for (const QweightKernel *k : kQweight) {
         const bool rows_fit = k->bm == 64 ? rows >= 512 : k->bm == 32 ? rows > 16 : k->bm == 16;
-        if (rows_fit && ceil_div(d->N, k->bn) >= ceil_div(want, row_tiles(d, offsets, *k)))
-            return k;
+        if (!rows_fit || ceil_div(d->N, k->bn) < ceil_div(want, row_tiles(d, offsets, *k)))
+            continue;
+        const int64_t rt = row_tiles(d, offsets, *k);
+        const bool fewer = 7 * chip_passes(rt, d->N, 512) < 4 * chip_passes(rt, d->N, 256);
+        return k == &kQ64x256 && wide && fewer ? &kQ64x512 : k;
     }
     return &kQ16x16;
 }

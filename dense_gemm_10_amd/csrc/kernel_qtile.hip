@@ -8,4 +8,11 @@ hipError_t launch_qweight_tile(const QweightArgs &a, uint32_t programs, hipStrea
     return launch_shape<4, 2, 8, 1, 2, 64>(a, programs, s);
 }
 
+// Group sizes that are multiples of 128 only: with more scales in a panel
+// the eight wavefronts' sums do not fit into registers.
+hipError_t launch_qweight_wide_tile(const QweightArgs &a, uint32_t programs, hipStream_t s)
+{
+    return launch_scaled<4, 4, 4, 8, 1, 1, 64>(a, programs, s);
+}
+
 } // namespace dg

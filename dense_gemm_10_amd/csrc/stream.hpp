@@ -77,38 +77,6 @@ __device__ __forceinline__ void stream_store(const GemmArgs &g, int64_t m0, int6
     }
 }
 
-// Steps 0 .. n - 1 of a wavefront with D of them in registers: step i + D is
-// loaded as soon as step i has been multiplied.  The steady loop has no
-// branch, so the compiler's waits leave the younger steps' loads in flight.
-template <int D, typename Step, typename Load, typename Multiply>
-__device__ __forceinline__ void stream_steps(uint32_t n, Load &&load, Multiply &&multiply)
-{
-    Step ring[D];
-#pragma unroll
-    for (uint32_t d = 0; d < D; ++d)
-        if (d < n)
-            load(ring[d], d);
-    uint32_t i = 0;
-    for (; i + 2 * D <= n; i += D) {
-#pragma unroll
-        for (uint32_t d = 0; d < D; ++d) {
-            multiply(ring[d]);
-            load(ring[d], i + d + D);
-        }
-    }
-#pragma unroll
-    for (uint32_t d = 0; d < D; ++d)
-        if (i + d < n) {
-            multiply(ring[d]);
-            if (i + d + D < n)
-                load(ring[d], i + d + D);
-        }
-#pragma unroll
-    for (uint32_t d = 0; d < D; ++d)
-        if (i + D + d < n)
-            multiply(ring[d]);
-}
-
 template <int FM, int FN, int KW>
 constexpr size_t stream_lds_bytes() { return (size_t)KW * 16 * FM * (16 * FN + 4) * 4; }
 

@@ -32,6 +32,10 @@ hipError_t launch_qweight_tile(const QweightArgs &, uint32_t, hipStream_t)
 {
     return hipErrorInvalidValue;
 }
+hipError_t launch_qweight_wide_tile(const QweightArgs &, uint32_t, hipStream_t)
+{
+    return hipErrorInvalidValue;
+}
 hipError_t launch_qweight_generic(const QweightArgs &, uint32_t, hipStream_t)
 {
     return hipErrorInvalidValue;

@@ -178,7 +178,8 @@ def test_kernel_of_a_grouped_problem(kw, kernel, monkeypatch):
     (1, 4096, 4096, 128, {}, "qstream_16x16"), (1, 16384, 8192, 64, {}, "qstream_16x32"),
     (16, 16384, 4096, 128, {}, "qstream_16x64"), (64, 4096, 4096, 128, {}, "qstream_32x32"),
     (128, 4096, 4096, 128, {}, "qstream_32x64"), (512, 4096, 4096, 128, {}, "qstream_32x128"),
-    (2048, 4096, 4096, 128, {}, "qtile_64x256"), (5, 64, 4112, 128, {}, "generic"),
+    (2048, 4096, 4096, 128, {}, "qtile_64x512"), (1024, 4096, 4096, 128, {}, "qtile_64x256"),
+    (2048, 4096, 4096, 64, {}, "qtile_64x256"), (5, 64, 4112, 128, {}, "generic"),
     (5, 64, 128, 32, dict(ldq=72), "generic"), (5, 64, 128, 32, dict(lda=132), "generic"),
     (64, 2048, 2048, 128, dict(groups=64), "qstream_16x64"),
     (64, 2048, 2048, 128, dict(groups=64, stride_q=2048 * 1024 + 8), "generic"),

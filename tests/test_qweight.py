@@ -180,20 +180,21 @@ def test_nan_rows_and_scales_stay_where_they_are(M):
 
 
 @pytest.mark.parametrize("kernel", ["qstream_16x16", "qstream_16x32", "qstream_16x64", "qstream_32x32",
-                                    "qstream_32x64", "qstream_32x128", "qtile_64x256"])
+                                    "qstream_32x64", "qstream_32x128", "qtile_64x256", "qtile_64x512"])
 def test_every_kernel(kernel, monkeypatch):
     """The kernel depends on the sizes alone; each is right for any rows,
     columns, K, group size and lengths."""
     monkeypatch.setenv("DG_FORCE_GROUPED", kernel)
     gen = torch.Generator().manual_seed(17)
     for M, N, K, g, dt, with_zeros in ((1, 300, 4384, 128, torch.bfloat16, False), (70, 130, 288, 96, torch.float16, True),
-                                       (33, 16, 64, 64, torch.bfloat16, True), (130, 520, 1056, 32, torch.float16, False)):
+                                       (33, 16, 64, 64, torch.bfloat16, True), (130, 520, 1056, 32, torch.float16, False),
+                                       (130, 1040, 1056, 256, torch.bfloat16, True)):
         q, scales, zeros = _make(gen, (), N, K, g, dt, with_zeros, True)
         A = ints(gen, M, K, dtype=dt)
         got = dg.gemm_qweight(A.cuda(), _pack(q).cuda(), scales.cuda(), _dev(zeros), group_size=g,
                               out_dtype=torch.float32)
         assert torch.equal(got.cpu().double(), A.double() @ _weights(q, scales, zeros, g).t()), (M, N, K)
-    groups, rows, N, K, g = 70, 300, 72, 192, 64
+    groups, rows, N, K, g = 70, 300, 72, 192, 128 if kernel == "qtile_64x512" else 64
     q, scales, zeros = _make(gen, (groups,), N, K, g, torch.bfloat16, True, True)
     A, W = ints(gen, rows, K, dtype=torch.bfloat16), _weights(q, scales, zeros, g)
     for pattern in ("random", "one", "edges"):
