@@ -213,10 +213,13 @@ bool mfma_ok(const dg_grouped_desc *d, const void *A, const void *B)
 //     305-313 against 390-418; 2000 rows, 16 groups, 4096 x 2048: 78 against
 //     103; but 1000 rows, 4 groups, 4096 x 1024, 28 tiles: 61-73 against
 //     49-51, and 6000 rows, 48 groups, 512 x 1024: 32 against 27).
-// Ragged K: the 128 x 128 tile, whose second workgroup on a CU covers the
-// other's epilogue (16 groups of 2048 x 2048, 8192 rows: 103 against 107;
-// 32 of 512 x 1024: 18-21 against 24), unless the groups are long and 256 x
-// 256 tiles fill the chip (8 of 1024 x 2048: 47 against 50).
+// Ragged K: the 128 x 128 tile, whose other workgroups on a CU cover one's
+// epilogue (16 groups of 2048 x 2048, 8192 rows: 102 against 112; 32 of 512
+// x 1024: 24 against 29), unless the groups are long and 256 x 256 tiles fill
+// the chip twice, so that long and short groups even out (16384 rows, 8
+// groups, 4096 x 4096: 505 against 585, 2048 x 2048: 167 against 185; but
+// 8192 rows, 1024 x 2048, 256 tiles: 58 against 52), or once with one group
+// (4096 rows, 4096 x 4096: 120 against 133).
 const GroupedKernel *choose(const dg_grouped_desc *d, const void *A, const void *B)
 {
     if (!mfma_ok(d, A, B))
@@ -231,7 +234,7 @@ const GroupedKernel *choose(const dg_grouped_desc *d, const void *A, const void 
     const double n256 = (double)ceil_div(d->N, 256);
     if (rk) {
         const double tiles = (double)d->groups * (double)ceil_div(d->M, 256) * n256;
-        return mean >= 768 && tiles >= 240 ? &kTile256 : &kTile128;
+        return mean >= 768 && tiles >= (d->groups > 1 ? 480 : 240) ? &kTile256 : &kTile128;
     }
     if (mean <= 8)
         return row_tiles(d->rows, d->groups, 16) * ceil_div(d->N, 64) < 512 ? &kStream16x32

@@ -353,6 +353,20 @@ def test_every_kernel_takes_every_pattern(kernel, monkeypatch):
             assert torch.equal(got.cpu().double(), _ref_k(A.t(), G, off, torch.float32)[0])
 
 
+@pytest.mark.parametrize("kernel", ["mfma16_256x256", "mfma16_128x128"])
+@pytest.mark.parametrize("M,N", [(520, 648), (136, 3080), (3080, 136)])
+def test_weight_gradient_of_many_tiles(kernel, M, N, monkeypatch):
+    """More tiles than the chip holds at once, in bands that end anywhere."""
+    monkeypatch.setenv("DG_FORCE_GROUPED", kernel)
+    gen = torch.Generator().manual_seed(M + N)
+    groups, rows = 60, 700
+    A, G = ints(gen, rows, M, dtype=torch.bfloat16), ints(gen, rows, N, dtype=torch.bfloat16)
+    off = offsets_like("random", groups, rows, gen)
+    got = dg.gemm_grouped_k(A.cuda().t(), G.cuda(), _offsets(off), out_dtype=torch.float32).cpu()
+    for e, (lo, hi) in enumerate(groups_of(off, rows)):
+        assert torch.equal(got[e], A[lo:hi].float().t() @ G[lo:hi].float()), e
+
+
 def test_runs_repeat_bit_for_bit():
     gen = torch.Generator().manual_seed(6)
     groups, rows, K, N = 6, 500, 264, 264

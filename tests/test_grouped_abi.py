@@ -159,7 +159,9 @@ def _kernel(text):
     (dict(groups=4, rows=100, K=64, N=64, stride_b=4100), "generic"),
     (dict(groups=1, rows=100, K=64, N=64, stride_b=4100), "mfma16_128x128"),
     (dict(ragged="k", groups=16, rows=8192, M=2048, N=2048), "mfma16_128x128"),
-    (dict(ragged="k", groups=8, rows=8192, M=1024, N=2048), "mfma16_256x256"),
+    (dict(ragged="k", groups=8, rows=8192, M=1024, N=2048), "mfma16_128x128"),
+    (dict(ragged="k", groups=8, rows=16384, M=2048, N=2048), "mfma16_256x256"),
+    (dict(ragged="k", groups=1, rows=4096, M=4096, N=4096), "mfma16_256x256"),
     (dict(ragged="k", groups=8, rows=8192, M=1024, N=2048, a_type="f32"), "mfma_f32_128x128"),
     (dict(ragged="k", groups=8, rows=8192, M=1001, N=2048), "generic"),
 ], ids=str)
