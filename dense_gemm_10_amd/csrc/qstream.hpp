@@ -15,6 +15,13 @@
 // Nothing is rounded to 16 bits; the subtraction costs the sums at most
 // five bits of fp32 (|16 + q| <= 31 against |q - zero| of a few units).
 //
+// Measured (MI355X): one row through 16384 x 8192 (fp16, groups of 64) 17.4
+// us, 4.2 TB/s, bound by the codes' bytes; through 4096 x 4096 5.4 us in a
+// replayed graph, 7.8 us called from the host, bound by launch and latency;
+// 2048 rows through 4096 x 4096 (bf16, groups of 128) 100 us, 0.69 PFLOP/s,
+// bound by turning codes into operands and by their scales' fp32 arithmetic,
+// which share the issue slots with the matrix instructions.
+//
 // Work split.  A workgroup is NW x KW wavefronts and owns 16 FM rows x 16
 // FN NW columns; it walks K in panels of 128 KW TS.  Per panel the
 // workgroup stages A's rows (MR <= 16 FM at most) and the panel's scales in LDS, and wavefront

