@@ -367,6 +367,16 @@ def test_weight_gradient_of_many_tiles(kernel, M, N, monkeypatch):
         assert torch.equal(got[e], A[lo:hi].float().t() @ G[lo:hi].float()), e
 
 
+def test_weight_gradient_of_many_tiles_and_long_groups():
+    gen = torch.Generator().manual_seed(12)
+    groups, rows, M, N = 5, 2400, 1928, 1800
+    A, G = ints(gen, rows, M, dtype=torch.bfloat16), ints(gen, rows, N, dtype=torch.bfloat16)
+    off = [0, 1500, 1500, 1533, 2399, 2400]
+    got = dg.gemm_grouped_k(A.cuda().t(), G.cuda(), _offsets(off), out_dtype=torch.float32).cpu()
+    for e, (lo, hi) in enumerate(groups_of(off, rows)):
+        assert torch.equal(got[e], A[lo:hi].float().t() @ G[lo:hi].float()), e
+
+
 def test_runs_repeat_bit_for_bit():
     gen = torch.Generator().manual_seed(6)
     groups, rows, K, N = 6, 500, 264, 264
