@@ -357,17 +357,18 @@ int64_t chip_passes(int64_t row_tiles, int64_t n, int64_t bn)
 {
     const int64_t per_pass = 256, cols = ceil_div(n, bn);
     if (row_tiles > INT64_MAX / cols)
-        return INT64_MAX / 8;
+        return INT64_MAX / 8;       // not reached for a grid that can be launched
     return ceil_div(row_tiles * cols, per_pass);
 }
 
-// From 512 rows a group, if 64 x 256 tiles fill the chip, the tile (us, 4096
-// x 4096, bf16, group size 128): 1024 rows 58 against 67, 2048 rows 115
-// against 130; below, it does not (256 rows: 54 against 24).  A pass of 64 x 512
-// tiles over the chip takes 98 us where one of 64 x 256 takes 57 (four
-// column blocks per wavefront read a row of A once, but hold 256 registers),
-// so they are taken where they need less than 4/7 of the passes: 2048 rows
-// 102 against 112, 8192 x 8192 370 against 409; 1024 rows 98 against 57.
+// From 256 rows a group, if 64 x 256 tiles fill the chip, the tile (us, 4096
+// x 4096, bf16, group size 128): 1024 rows 48 against 62, 2048 rows 95
+// against 120; 256 rows of 14336 x 4096 49 against 64; where they do not, it
+// loses (256 rows of 4096 x 4096: 46 against 23).  A pass of 64 x 512 tiles
+// over the chip takes 78-84 us where one of 64 x 256 takes 47 (four column
+// blocks per wavefront read a row of A once, but hold 256 registers), so they
+// are taken where they need less than 3/5 of the passes: 2048 rows 84 against
+// 95, 8192 x 8192 311 against 344; 1024 rows 78 against 48.
 // Else 32 rows where a group has more than 16, and the widest workgroup
 // (each reads A once) that still makes 512 of them for up to 4 rows, 256
 // for more, where A's traffic counts:
@@ -375,7 +376,7 @@ int64_t chip_passes(int64_t row_tiles, int64_t n, int64_t bn)
 //            16384 x 4096: 12.5, 10.2, 11.8;  8192 x 8192: 10.5, 12.6, 19.1
 //   16 rows, 4096 x 4096: 7.2, 9.2, 11.8;  16384 x 4096: 18.6, 14.0, 13.3
 //   64 rows, 16384 x 4096: 31.8 on 16 x 64, 31.6 on 32 x 32, 26.9 on 32 x 64
-//   512 rows, 4096 x 4096: 60.5 on 32 x 32, 44.9 on 32 x 64, 35.5 on 32 x
+//   512 rows, 4096 x 4096: 60.5 on 32 x 32, 44.9 on 32 x 64, 34.4 on 32 x
 //     128 (two column blocks per wavefront halve its reads of A from LDS)
 const QweightKernel *choose(const dg_qweight_desc *d, bool offsets, const void *A, const void *Q)
 {
@@ -390,11 +391,11 @@ const QweightKernel *choose(const dg_qweight_desc *d, bool offsets, const void *
     const int64_t rows = offsets ? d->M / d->groups : d->M;
     const int64_t want = rows <= 4 ? 512 : 256;
     for (const QweightKernel *k : kQweight) {
-        const bool rows_fit = k->bm == 64 ? rows >= 512 : k->bm == 32 ? rows > 16 : k->bm == 16;
+        const bool rows_fit = k->bm == 64 ? rows >= 256 : k->bm == 32 ? rows > 16 : k->bm == 16;
         if (!rows_fit || ceil_div(d->N, k->bn) < ceil_div(want, row_tiles(d, offsets, *k)))
             continue;
         const int64_t rt = row_tiles(d, offsets, *k);
-        const bool fewer = 7 * chip_passes(rt, d->N, 512) < 4 * chip_passes(rt, d->N, 256);
+        const bool fewer = 5 * chip_passes(rt, d->N, 512) < 3 * chip_passes(rt, d->N, 256);
         return k == &kQ64x256 && wide && fewer ? &kQ64x512 : k;
     }
     return &kQ16x16;

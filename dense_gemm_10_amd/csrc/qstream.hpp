@@ -18,9 +18,9 @@
 // Measured (MI355X): one row through 16384 x 8192 (fp16, groups of 64) 17.4
 // us, 4.2 TB/s, bound by the codes' bytes; through 4096 x 4096 5.4 us in a
 // replayed graph, 7.8 us called from the host, bound by launch and latency;
-// 2048 rows through 4096 x 4096 (bf16, groups of 128) 100 us, 0.69 PFLOP/s,
-// bound by turning codes into operands and by their scales' fp32 arithmetic,
-// which share the issue slots with the matrix instructions.
+// 2048 rows through 4096 x 4096 (bf16, groups of 128) 84 us, 0.82 PFLOP/s,
+// bound by the panel's chain of stage, barrier and first operand reads, which
+// two wavefronts per SIMD do not cover.
 //
 // Work split.  A workgroup is NW x KW wavefronts and owns 16 FM rows x 16
 // FN NW columns; it walks K in panels of 128 KW TS.  Per panel the
@@ -42,6 +42,7 @@
 // that are multiples of 32, 64 or 128).
 #pragma once
 #include "stream.hpp"
+#include <type_traits>
 
 namespace dg {
 
@@ -160,6 +161,7 @@ struct QPanel {
     static constexpr int A_PER = MR * K / 8 / NT;         // 16-byte pieces of A per thread
     static constexpr int S_ALL = COLS * E;                // scales of the panel
     static constexpr int S_PER = (S_ALL + NT - 1) / NT;   // ... per thread
+    static constexpr int PIECES = A_PER + S_PER;          // loads of a thread for a panel
     static constexpr int SUM_LD = COLS + 4;
     static constexpr int SUM_AT = (A_BYTES + COLS * S_LD * 8 + 15) / 16 * 16;   // sums[E][16 FM]
     static constexpr bool STAGED_SUMS = FN > 1;
@@ -228,50 +230,58 @@ void qweight_stream_kernel(QweightArgs a, FastDiv by_group)
     };
     struct Staged {
         uint4 a[P::A_PER];
-        uint32_t s[P::S_PER];
-        uint32_t z[P::S_PER];
+        // as loaded: widened here, they would have to arrive first
+        std::conditional_t<S32, uint32_t, uint16_t> s[P::S_PER];
+        uint8_t z[P::S_PER];
     };
     // k past K reads the row's last codes: A is zero there.
+    auto load_code = [&](Codes &r, uint32_t k0, int i, int j) {
+        const uint32_t k = k0 + (kw + i * KW) * QK + 32 * kg;
+        r.q[i][j] = load16_at(qb, qo[j] + (k < K ? k : K - 32) / 2);
+    };
     auto load_codes = [&](Codes &r, uint32_t k0) {
 #pragma unroll
-        for (int i = 0; i < TS; ++i) {
-            const uint32_t k = k0 + (kw + i * KW) * QK + 32 * kg;
-            const uint32_t at = (k < K ? k : K - 32) / 2;
+        for (int i = 0; i < TS; ++i)
 #pragma unroll
             for (int j = 0; j < FN; ++j)
-                r.q[i][j] = load16_at(qb, qo[j] + at);
-        }
+                load_code(r, k0, i, j);
     };
-    auto load_panel = [&](Staged &r, uint32_t k0) {
-#pragma unroll
-        for (int i = 0; i < P::A_PER; ++i) {
-            const int piece = tid + i * P::NT, row = piece / (P::K / 8);
+    // one piece per thread of the panel: 0 .. A_PER - 1 of A, then of the scales
+    auto load_piece = [&](Staged &r, uint32_t k0, int p) {
+        if (p < P::A_PER) {
+            const int piece = tid + p * P::NT, row = piece / (P::K / 8);
             const uint32_t k = k0 + piece % (P::K / 8) * 8;
             // few rows: no load for those that are not there; many: the last
             // row again, without a branch
             if (P::TWO || (row < rows && k < K))
-                r.a[i] = load16_at(ab, (uint32_t)(row < rows ? row : rows - 1) * (uint32_t)(2 * a.lda) +
+                r.a[p] = load16_at(ab, (uint32_t)(row < rows ? row : rows - 1) * (uint32_t)(2 * a.lda) +
                                            2 * (k < K ? k : 0));
-        }
-#pragma unroll
-        for (int i = 0; i < P::S_PER; ++i) {
+        } else {
+            const int i = p - P::A_PER;
             const int all = tid + i * P::NT, e = all < P::S_ALL ? all : P::S_ALL - 1;
             const int n = e / P::E;
             const uint32_t k = k0 + e % P::E * (32 * SPG);
             const uint32_t at = (uint32_t)(n < cols ? n : cols - 1) * (uint32_t)a.lds +
                                 fastdiv(k < K ? k : K - 1, by_group);
-            r.s[i] = S32 ? load_at<uint32_t>(sb, at * 4) : load_at<uint16_t>(sb, at * 2);
+            if constexpr (S32)
+                r.s[i] = load_at<uint32_t>(sb, at * 4);
+            else
+                r.s[i] = load_at<uint16_t>(sb, at * 2);
             if (ZEROS)
                 r.z[i] = load_at<uint8_t>(zb, at);
         }
     };
-    const bool f16_scale = a.scale_type == DT_F16;
-    auto store_panel = [&](const Staged &r, uint32_t k0, int b) {
+    auto load_panel = [&](Staged &r, uint32_t k0) {
 #pragma unroll
-        for (int i = 0; i < P::A_PER; ++i) {
-            const int piece = tid + i * P::NT, row = piece / (P::K / 8), at = piece % (P::K / 8) * 8;
+        for (int p = 0; p < P::PIECES; ++p)
+            load_piece(r, k0, p);
+    };
+    const bool f16_scale = a.scale_type == DT_F16;
+    auto store_piece = [&](const Staged &r, uint32_t k0, int b, int p) {
+        if (p < P::A_PER) {
+            const int piece = tid + p * P::NT, row = piece / (P::K / 8), at = piece % (P::K / 8) * 8;
             // one scale's pieces are 4 SPG consecutive lanes of one row
-            const uint4 v = k0 + at < K ? r.a[i] : make_uint4(0u, 0u, 0u, 0u);
+            const uint4 v = k0 + at < K ? r.a[p] : make_uint4(0u, 0u, 0u, 0u);
             float sum = 0.0f;
             if constexpr (P::STAGED_SUMS)
                 sum = run_sum<4 * SPG>(sum_of_piece<T>(v));
@@ -280,19 +290,24 @@ void qweight_stream_kernel(QweightArgs a, FastDiv by_group)
                 if (P::STAGED_SUMS && piece % (4 * SPG) == 0)
                     sum_lds(b)[at / (32 * SPG) * (16 * FM) + row] = sum;
             }
-        }
-#pragma unroll
-        for (int i = 0; i < P::S_PER; ++i) {
-            const int e = tid + i * P::NT;
-            float f = __uint_as_float(r.s[i]);
-            if (!S32)
-                f = f16_scale ? f16_to_f32((uint16_t)r.s[i]) : bf16_to_f32((uint16_t)r.s[i]);
+        } else {
+            const int i = p - P::A_PER, e = tid + i * P::NT;
+            float f;
+            if constexpr (S32)
+                f = __uint_as_float(r.s[i]);
+            else
+                f = f16_scale ? f16_to_f32(r.s[i]) : bf16_to_f32(r.s[i]);
             const float h = ZEROS ? -16.0f - (float)(r.z[i] & 15) : -24.0f;
             // past K a scale of zero: the sums there are zero, whatever the scale
             const bool in = k0 + e % P::E * (32 * SPG) < K;
             if (e < P::S_ALL)
                 s_lds(b)[e / P::E * P::S_LD + e % P::E] = make_float2(in ? f : 0.0f, h);
         }
+    };
+    auto store_panel = [&](const Staged &r, uint32_t k0, int b) {
+#pragma unroll
+        for (int p = 0; p < P::PIECES; ++p)
+            store_piece(r, k0, b, p);
     };
 
     const f32x4_t none{0.0f, 0.0f, 0.0f, 0.0f};
@@ -311,7 +326,10 @@ void qweight_stream_kernel(QweightArgs a, FastDiv by_group)
         a_at[i] = (16 * i + c < rows ? 16 * i + c : rows - 1) * P::A_LD + 8 * kg;
     const int s_at = (16 * FN * nw + c) * P::S_LD;
 
-    auto multiply = [&](const Codes &r, int b, uint32_t k0) {
+    // `between(slot)` is called after each column block's MFMAs, slots 0 ..
+    // SLOTS - 1 of a panel
+    constexpr int SLOTS = TS * 4 * FN;
+    auto multiply = [&](const Codes &r, int b, uint32_t k0, auto &&between) {
         const uint16_t *a_buf = a_lds(b);
         const float2 *s_row = s_lds(b) + s_at;
         const float *sums = sum_lds(b) + 4 * kg;
@@ -358,6 +376,7 @@ void qweight_stream_kernel(QweightArgs a, FastDiv by_group)
 #pragma unroll
                     for (int x = 0; x < FM; ++x)
                         u[x][j] = mfma_16x16x32(af[x], b, first ? none : u[x][j]);
+                    between((4 * i + m) * FN + j);
                 }
                 if (m % SPG == SPG - 1) {
                     sched_fence();
@@ -395,13 +414,28 @@ void qweight_stream_kernel(QweightArgs a, FastDiv by_group)
             for (uint32_t k0 = 0;; b ^= 1) {
                 const uint32_t k1 = k0 + P::K;
                 if (k1 >= K) {
-                    multiply(now, b, k0);
+                    multiply(now, b, k0, [](int) {});
                     break;
                 }
-                store_panel(panel, k1, b ^ 1);
-                load_codes(next, k1);
-                load_panel(panel, k1 + P::K);
-                multiply(now, b, k0);
+                // The next panel's codes, the staging of its rows and scales
+                // and the loads of the panel after it, one at a time between
+                // the MFMAs: in one block before them they keep the matrix
+                // pipe waiting for the issue of the 8 wavefronts' loads (2048
+                // rows of 4096 x 4096: 98 us, in one block 104).
+                multiply(now, b, k0, [&](int slot) {
+                    constexpr int JOBS = TS * FN + P::PIECES;
+#pragma unroll
+                    for (int job = 0; job < JOBS; ++job) {
+                        if (job * SLOTS / JOBS != slot)
+                            continue;
+                        if (job < TS * FN) {
+                            load_code(next, k1, job / FN, job % FN);
+                        } else {
+                            store_piece(panel, k1, b ^ 1, job - TS * FN);
+                            load_piece(panel, k1 + P::K, job - TS * FN);
+                        }
+                    }
+                });
                 lds_barrier();
                 now = next;
                 k0 = k1;
@@ -411,12 +445,12 @@ void qweight_stream_kernel(QweightArgs a, FastDiv by_group)
             for (uint32_t k0 = 0;;) {
                 const uint32_t k1 = k0 + P::K;
                 if (k1 >= K) {
-                    multiply(now, 0, k0);
+                    multiply(now, 0, k0, [](int) {});
                     break;
                 }
                 load_panel(panel, k1);
                 load_codes(next, k1);
-                multiply(now, 0, k0);
+                multiply(now, 0, k0, [](int) {});
                 lds_barrier();             // every wavefront is done with this panel
                 store_panel(panel, k1, 0);
                 lds_barrier();
@@ -450,15 +484,47 @@ void qweight_stream_kernel(QweightArgs a, FastDiv by_group)
                 part[(kw * 16 * FM + 16 * i + 4 * kg + v) * P::SUM_LD + 16 * (FN * nw + j) + c] =
                     acc[i][j][v];
     lds_barrier();
-    for (int o = tid; o < 16 * FM * P::COLS; o += P::NT) {
-        const int r = o / P::COLS, n = o % P::COLS;
+    // Large tiles: four columns per thread, one store each, where C's rows
+    // allow it (2048 rows of 4096 x 4096: 85 us, one by one 98).
+    constexpr int RUN = 16 * FM * P::COLS >= 8 * P::NT ? 4 : 1;
+    const int cs = a.c_type == DT_F32 ? 4 : 2;
+    const bool whole = RUN > 1 && a.ldc % RUN == 0 && (uintptr_t)g.C % (RUN * cs) == 0;
+    for (int o = tid; o < 16 * FM * P::COLS / RUN; o += P::NT) {
+        const int r = o / (P::COLS / RUN), n = o % (P::COLS / RUN) * RUN;
         if (r >= rows || n >= cols)
             continue;
-        float sum = 0.0f;
+        float v[RUN];
 #pragma unroll
-        for (int w = 0; w < KW; ++w)
-            sum += part[(w * 16 * FM + r) * P::SUM_LD + n];
-        store_c(g, 0, m0 + r, n0 + n, epilogue_value(g, 0, m0 + r, n0 + n, sum));
+        for (int e = 0; e < RUN; ++e) {
+            v[e] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < KW; ++w)
+                v[e] += part[(w * 16 * FM + r) * P::SUM_LD + n + e];
+        }
+        if constexpr (RUN > 1) {
+            if (whole && n + RUN <= cols) {
+                float bias[RUN];
+#pragma unroll
+                for (int e = 0; e < RUN; ++e)
+                    bias[e] = g.bias ? load_as_f32(g.bias, g.bias_type, n0 + n + e) : 0.0f;
+                run_epilogue<RUN>(g, 0, m0 + r, n0 + n, g.N, false, v, bias);
+                char *dst = (char *)g.C + ((m0 + r) * g.ldc + n0 + n) * cs;
+                if (g.c_type == DT_F32) {
+                    store16(dst, v[0], v[1], v[2], v[3]);
+                } else {
+                    uint32_t h[RUN];
+#pragma unroll
+                    for (int e = 0; e < RUN; ++e)
+                        h[e] = g.c_type == DT_F16 ? f32_to_f16(v[e]) : f32_to_bf16(v[e]);
+                    *(uint2 *)dst = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+                }
+                continue;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < RUN; ++e)
+            if (n + e < cols)
+                store_c(g, 0, m0 + r, n0 + n + e, epilogue_value(g, 0, m0 + r, n0 + n + e, v[e]));
     }
 }
 
