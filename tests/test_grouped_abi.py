@@ -231,3 +231,14 @@ OFF5 = torch.zeros(5, dtype=torch.int32)
 def test_torch_entry_points_refuse(what, call, match):
     with pytest.raises(ValueError, match=match):
         call()
+
+
+def test_packed_descriptors_match_the_structures():
+    """The torch entry points pack the descriptors' bytes directly."""
+    from dense_gemm_10_amd import grouped as G
+    ints = list(range(1, 19))
+    for cls, pack, size in ((G.DgGroupedDesc, G._pack_grouped, G._GROUPED_SIZE),
+                            (G.DgQweightDesc, G._pack_qweight, G._QWEIGHT_SIZE)):
+        n = len(cls._fields_) - 4
+        values = [size, *ints[:n], 1.5, -0.25, 0x1234567890]
+        assert pack(*values) == bytes(cls(*values))
