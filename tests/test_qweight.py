@@ -208,6 +208,30 @@ def test_every_kernel(kernel, monkeypatch):
         assert torch.equal(C.cpu().double(), ref), pattern
 
 
+@pytest.mark.parametrize("kernel", ["qstream_32x128", "qtile_64x256", "qtile_64x512"])
+@pytest.mark.parametrize("out,scale", [("bf16", "f32"), ("f16", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("first,pad", [(0, 2), (4, 2), (2, 0), (1, 3), (0, 1)])
+def test_output_at_any_alignment(kernel, out, scale, first, pad, monkeypatch):
+    """C a part of a wider matrix: rows on four columns or not; nothing
+    beside it is written."""
+    monkeypatch.setenv("DG_FORCE_GROUPED", kernel)
+    gen = torch.Generator().manual_seed(first + pad)
+    M, N, K, g = 75, 522, 416, 128
+    q, scales, zeros = _make(gen, (), N, K, g, DT[scale], True, False)
+    A, bias = torch.randn(M, K, generator=gen).bfloat16(), torch.randn(N, generator=gen).bfloat16()
+    y, err = A.double() @ _weights(q, scales, zeros, g).t(), _error(A, q, scales, zeros, g, K)
+    wide = torch.randn(M, first + N + pad, generator=gen).to(DT[out])
+    for beta, b, act in ((0.0, None, "none"), (1.0, bias, "gelu_erf")):
+        W = wide.cuda()
+        C = W[:, first:first + N]
+        dg.gemm_qweight(A.cuda(), _pack(q).cuda(), scales.cuda(), zeros.cuda(), C, group_size=g,
+                        beta=beta, bias=_dev(b), act=act)
+        ref, tol = finish(y, None, err, DT[out], beta=beta, C=wide[:, first:first + N], bias=b, act=act)
+        check(C, ref, tol, f"{beta} {act}")
+        assert torch.equal(W[:, :first].cpu(), wide[:, :first])
+        assert torch.equal(W[:, first + N:].cpu(), wide[:, first + N:])
+
+
 def test_empty_sizes():
     def z(*shape, dtype=torch.bfloat16):
         return torch.zeros(shape, dtype=dtype, device="cuda")
