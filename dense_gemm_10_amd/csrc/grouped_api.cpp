@@ -376,7 +376,7 @@ int64_t chip_passes(int64_t row_tiles, int64_t n, int64_t bn)
 //            16384 x 4096: 12.5, 10.2, 11.8;  8192 x 8192: 10.5, 12.6, 19.1
 //   16 rows, 4096 x 4096: 7.2, 9.2, 11.8;  16384 x 4096: 18.6, 14.0, 13.3
 //   64 rows, 16384 x 4096: 31.8 on 16 x 64, 31.6 on 32 x 32, 26.9 on 32 x 64
-//   512 rows, 4096 x 4096: 60.5 on 32 x 32, 44.9 on 32 x 64, 34.4 on 32 x
+//   512 rows, 4096 x 4096: 60.5 on 32 x 32, 44.9 on 32 x 64, 33 on 32 x
 //     128 (two column blocks per wavefront halve its reads of A from LDS)
 const QweightKernel *choose(const dg_qweight_desc *d, bool offsets, const void *A, const void *Q)
 {

@@ -166,8 +166,11 @@ struct QPanel {
     static constexpr int SUM_AT = (A_BYTES + COLS * S_LD * 8 + 15) / 16 * 16;   // sums[E][16 FM]
     static constexpr bool STAGED_SUMS = FN > 1;
     static constexpr int PANEL = (SUM_AT + (STAGED_SUMS ? E * 16 * FM * 4 : 0) + 15) / 16 * 16;
-    // two panels in LDS, with one barrier each, where they are small
-    static constexpr bool TWO = FM >= 4;
+    // Two panels in LDS, with one barrier each, where a wavefront has four
+    // blocks or more (128 rows of 8192 x 8192 on 32 x 128: 40 us, with one
+    // panel 43); smaller ones live from many workgroups per CU, which two
+    // panels halve (512 rows of 4096 x 4096 on 32 x 32: 74 us against 55).
+    static constexpr bool TWO = FM * FN >= 4;
     static constexpr int LOOP = TWO ? 2 * PANEL : PANEL;
     static constexpr int STORE = KW * 16 * FM * SUM_LD * 4;
     static constexpr int BYTES = LOOP > STORE ? LOOP : STORE;
