@@ -1,0 +1,99 @@
+"""4-bit weights on every kernel where A holds NaN, infinities or subnormals."""
+import pytest
+import torch
+
+import dense_gemm_10_amd as dg
+from grouped_util import ints
+
+pytestmark = pytest.mark.gpu
+
+KERNELS = ["qstream_16x16", "qstream_16x32", "qstream_16x64", "qstream_32x32", "qstream_32x64",
+           "qstream_32x128", "qtile_64x256", "qtile_64x512"]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def _pack(q):
+    return q[..., 0::2] | (q[..., 1::2] << 4)
+
+
+def _weights(q, scales, zeros, g):
+    at = torch.arange(q.shape[-1]) // g
+    zero = 8.0 if zeros is None else zeros.double()[..., at]
+    return (q.double() - zero) * scales.double()[..., at]
+
+
+def _case(gen, lead, N, K, g, with_zeros, scale_dtype=torch.float32, low=-2):
+    """Codes, scales that are powers of two from 2^low, zeros."""
+    q = torch.randint(0, 16, (*lead, N, K), generator=gen, dtype=torch.uint8)
+    scales = 2.0 ** torch.randint(low, low + 4, (*lead, N, K // g), generator=gen)
+    zeros = torch.randint(0, 16, (*lead, N, K // g), generator=gen, dtype=torch.uint8) if with_zeros else None
+    return q, scales.to(scale_dtype), zeros
+
+
+def _dev(t):
+    return None if t is None else t.cuda()
+
+
+def _forced(kernel, monkeypatch, M, N, K, g):
+    monkeypatch.setenv("DG_FORCE_GROUPED", kernel)
+    got = dg.dg_gemm_qweight_describe(dg.make_qweight_desc(M, N, K, g))
+    assert f"kernel={kernel} " in got
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("g", [32, 64, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_nan_stays_in_its_row_and_column(kernel, g, dtype, monkeypatch):
+    """A last row tile that is cut, NaN in its last row and in two others; a
+    column with an infinite and one with a NaN scale."""
+    if kernel == "qtile_64x512" and g % 128:
+        pytest.skip("taken for group sizes that are multiples of 128")
+    M, N, K = 70, 530, 1184
+    K -= K % g
+    _forced(kernel, monkeypatch, M, N, K, g)
+    gen = torch.Generator().manual_seed(g)
+    q, scales, zeros = _case(gen, (), N, K, g, dtype == torch.float16)
+    A = ints(gen, M, K, dtype=dtype)
+    ref = A.double() @ _weights(q, scales, zeros, g).t()
+    rows, cols = [1, 65, 69], [7, 529]
+    A[1, 5], A[65, K - 1], A[69, 0] = (float("nan"),) * 3
+    scales[7, 1], scales[529, 0] = float("inf"), float("nan")
+    got = dg.gemm_qweight(A.cuda(), _pack(q).cuda(), scales.cuda(), _dev(zeros), group_size=g,
+                          out_dtype=torch.float32).cpu().double()
+    keep = torch.ones(M, N, dtype=torch.bool)
+    keep[rows], keep[:, cols] = False, False
+    assert torch.equal(got[keep], ref[keep])
+    assert bool(got[rows].isnan().all()) and not bool(got[:, cols].isfinite().any())
+
+
+@pytest.mark.parametrize("kernel", KERNELS + ["generic"])
+@pytest.mark.parametrize("g", [32, 64, 128])
+@pytest.mark.parametrize("dtype,with_zeros", [(torch.float16, False), (torch.float16, True), (torch.bfloat16, True)])
+def test_subnormals(kernel, g, dtype, with_zeros, monkeypatch):
+    """Multiples of the type's smallest subnormal, scales that bring them
+    back: the products' absolute values add to less than 2^24 units, so every
+    product and sum is exact."""
+    if kernel == "qtile_64x512" and g % 128:
+        pytest.skip("taken for group sizes that are multiples of 128")
+    M, N, K = 67, 520, 768
+    if kernel == "generic":
+        K += 16                                # no whole step
+    else:
+        _forced(kernel, monkeypatch, M, N, K, g)
+    unit, normal, low = (2.0 ** -24, 2.0 ** -14, 20) if dtype == torch.float16 else (2.0 ** -133, 2.0 ** -126, 118)
+    gen = torch.Generator().manual_seed(g)
+    q = torch.randint(0, 16, (N, K), generator=gen, dtype=torch.uint8)
+    S = -(-K // g)
+    scales = (2.0 ** torch.randint(low, low + 2, (N, S), generator=gen).double()).float()
+    zeros = torch.randint(0, 16, (N, S), generator=gen, dtype=torch.uint8) if with_zeros else None
+    A = (torch.randint(-60, 61, (M, K), generator=gen).double() * unit).to(dtype)
+    A[5] = unit                                # one sign: the sums of A are large
+    A[6, ::2] = normal                         # the smallest normal beside subnormals
+    got = dg.gemm_qweight(A.cuda(), _pack(q).cuda(), scales.cuda(), _dev(zeros), group_size=g,
+                          out_dtype=torch.float32)
+    assert torch.equal(got.cpu().double(), A.double() @ _weights(q, scales, zeros, g).t())
