@@ -13,7 +13,8 @@
 // wavefront has one column block and the matrix pipe is idle anyway, and is
 // formed as A is staged, once per workgroup, where it has more.
 // Nothing is rounded to 16 bits; the subtraction costs the sums at most
-// five bits of fp32 (|16 + q| <= 31 against |q - zero| of a few units).
+// five bits of fp32 (|16 + q| <= 31 against |q - zero| of a few units), and an
+// output whose sums are not finite is formed again (defined_product).
 //
 // Measured (MI355X): one row through 16384 x 8192 (fp16, groups of 64) 17.4
 // us, 4.2 TB/s, bound by the codes' bytes; through 4096 x 4096 5.4 us in a
@@ -144,6 +145,33 @@ __device__ __forceinline__ float run_sum(float v)
     if (LANES >= 16)
         add(std::integral_constant<int, 0x140>{});     // 15 - lane in 16 lanes
     return v;
+}
+
+// One output from the definition, k by k in fp32, in the order of the kernel
+// that takes every operand: where U or S is not finite (an infinity in A, or
+// values whose 31-fold sum passes fp32), U - (16 + zero) S does not give what
+// the formula does.  x: the row of A; q, scales, zeros (null: 8): the
+// column's, from its first code.  K is a multiple of 32.  One thread per
+// output: 2048 rows of NaN through 4096 x 4096 take 135 us instead of 84, of
+// infinities that meet no weight of zero 59 ms.  Not inlined: in line it
+// changed the K loop's instructions (one token through 16384 x 8192: 18.0 us;
+// called 17.5, without it 17.4).  What the test for it costs: nothing to 1.5 %
+// (2048 rows of 4096 x 4096: 83.1 -> 84.3 us).
+template <int T>
+__device__ __noinline__ float defined_product(const uint16_t *x, const uint8_t *q, const void *scales,
+                                              const uint8_t *zeros, int32_t scale_type, uint32_t K,
+                                              uint32_t per_scale)
+{
+    float sum = 0.0f;
+#pragma unroll 1
+    for (uint32_t k = 0; k < K && sum == sum; k += 2) {        // NaN stays NaN
+        const uint32_t j = k / per_scale;
+        const float scale = load_as_f32(scales, scale_type, j);
+        const int32_t zero = zeros ? zeros[j] & 15 : 8, two = q[k / 2];
+        sum = fmaf(half_to_f32<T>(x[k]), (float)((two & 15) - zero) * scale, sum);
+        sum = fmaf(half_to_f32<T>(x[k + 1]), (float)((two >> 4) - zero) * scale, sum);
+    }
+    return sum;
 }
 
 // LDS of a workgroup: A's panel, rows 16 bytes apart in banks, the panel's
@@ -487,6 +515,13 @@ void qweight_stream_kernel(QweightArgs a, FastDiv by_group)
                 part[(kw * 16 * FM + 16 * i + 4 * kg + v) * P::SUM_LD + 16 * (FN * nw + j) + c] =
                     acc[i][j][v];
     lds_barrier();
+    auto from_definition = [&](int r, int n) {
+        const int64_t s_at = s0 + n * a.lds;
+        return defined_product<T>((const uint16_t *)a.A + (t.start + m0 + r) * a.lda,
+                                  a.Q + t.group * a.stride_q + (n0 + n) * a.ldq,
+                                  (const char *)a.scales + s_at * (S32 ? 4 : 2), ZEROS ? a.zeros + s_at : nullptr,
+                                  a.scale_type, K, (uint32_t)(a.group_size < a.K ? a.group_size : a.K));
+    };
     // Large tiles: four columns per thread, one store each, where C's rows
     // allow it (2048 rows of 4096 x 4096: 85 us, one by one 98).
     constexpr int RUN = 16 * FM * P::COLS >= 8 * P::NT ? 4 : 1;
@@ -503,6 +538,16 @@ void qweight_stream_kernel(QweightArgs a, FastDiv by_group)
 #pragma unroll
             for (int w = 0; w < KW; ++w)
                 v[e] += part[(w * 16 * FM + r) * P::SUM_LD + n + e];
+        }
+        float all = v[0];                      // not finite if one of the run is not
+#pragma unroll
+        for (int e = 1; e < RUN; ++e)
+            all += v[e];
+        if (__builtin_expect(!(fabsf(all) < INFINITY), 0)) {
+#pragma unroll
+            for (int e = 0; e < RUN; ++e)
+                if (n + e < cols && !(fabsf(v[e]) < INFINITY))
+                    v[e] = from_definition(r, n + e);
         }
         if constexpr (RUN > 1) {
             if (whole && n + RUN <= cols) {

@@ -294,8 +294,7 @@ def gemm_qweight(A, Q, scales, zeros=None, C=None, *, group_size, offsets=None, 
     ceil(K / group_size)); zeros: uint8 of the same shape and strides, or
     None for 8.  With offsets (int32, groups + 1, on the GPU), Q, scales,
     zeros and optionally bias have a leading dimension of groups, and each
-    row of A uses its group's weights; rows of no group are left alone.
-    An infinity in A gives NaN in its row."""
+    row of A uses its group's weights; rows of no group are left alone."""
     uint8 = sys.modules["torch"].uint8
     ashape, qshape, sshape = A.shape, Q.shape, scales.shape
     grouped = offsets is not None

@@ -360,10 +360,9 @@ dg_status dg_gemm_grouped_describe(const dg_grouped_desc *d, char *buf, size_t l
  * + e * stride_bias; the offsets as above, with M in the place of rows, and
  * rows of no group left as they were.  offsets may be NULL when groups == 1:
  * all M rows then use the one W.
- * W is never rounded to 16 bits: the scales and zeros enter in fp32.  The
- * sums over one scale's k hold up to 31 times A's values, so an infinity in
- * A, or values whose 31-fold sum passes fp32, give NaN where the formula
- * gives an infinity or less.
+ * W is never rounded to 16 bits: the scales and zeros enter in fp32.
+ * Infinities and NaN give what the formula does, from every kernel; an output
+ * that is not finite takes longer (its k one by one).
  *
  *   struct_size  sizeof(dg_qweight_desc).
  *   a_type       BF16 or F16 (F32: DG_ERROR_NOT_SUPPORTED).

@@ -97,3 +97,41 @@ def test_subnormals(kernel, g, dtype, with_zeros, monkeypatch):
     got = dg.gemm_qweight(A.cuda(), _pack(q).cuda(), scales.cuda(), _dev(zeros), group_size=g,
                           out_dtype=torch.float32)
     assert torch.equal(got.cpu().double(), A.double() @ _weights(q, scales, zeros, g).t())
+
+
+@pytest.mark.parametrize("kernel", KERNELS + ["generic"])
+@pytest.mark.parametrize("g", [32, 64, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("experts", [False, True])
+def test_infinities_and_large_values_follow_the_formula(kernel, g, dtype, experts, monkeypatch):
+    """Infinities in A and in the scales, and (bf16) rows whose products with
+    16 + q pass the largest fp32: the formula's infinity, NaN or value, the
+    same from every kernel."""
+    if kernel == "qtile_64x512" and g % 128:
+        pytest.skip("taken for group sizes that are multiples of 128")
+    M, N, K = 70, 530, 512
+    if kernel == "generic":
+        K += 16
+    else:
+        _forced(kernel, monkeypatch, M, N, K, g)
+    gen = torch.Generator().manual_seed(g)
+    lead, S = (3,) if experts else (), -(-K // g)
+    q = torch.randint(0, 16, (*lead, N, K), generator=gen, dtype=torch.uint8)
+    scales = 2.0 ** torch.randint(-9, -7, (*lead, N, S), generator=gen).float()
+    scales[..., 7, 1], scales[..., 300, 0], scales[..., 11, 0] = float("inf"), -float("inf"), 0.0
+    zeros = torch.randint(0, 16, (*lead, N, S), generator=gen, dtype=torch.uint8) if g == 64 else None
+    A = ints(gen, M, K, dtype=dtype)
+    inf = float("inf")
+    A[1, 5], A[65, K - 1], A[69, 0], A[69, 9], A[40, 3], A[40, 4] = inf, -inf, inf, -inf, -inf, float("nan")
+    if dtype == torch.bfloat16:                # (16 + q) A passes 2^128; the sums of W A are exact, below 2^126
+        A[30] = 2.0 ** 124 * (1 - 2 * (torch.arange(K) % 2))
+        A[68] = A[30]
+    off = [0, 31, 60, M] if experts else None
+    C = dg.gemm_qweight(A.cuda(), _pack(q).cuda(), scales.cuda(), _dev(zeros), group_size=g,
+                        offsets=None if off is None else torch.tensor(off, dtype=torch.int32, device="cuda"),
+                        out_dtype=torch.float32).cpu().double()
+    W = _weights(q, scales, zeros, g)
+    ref = A.double() @ W.t() if off is None else torch.cat(
+        [A[lo:hi].double() @ W[e].t() for e, (lo, hi) in enumerate(zip(off[:-1], off[1:]))])
+    assert bool(ref[30, 12:299].isfinite().all()) and bool(ref[1].isinf().any()) and bool(ref[1].isnan().any())
+    torch.testing.assert_close(C, ref, rtol=0, atol=0, equal_nan=True)
