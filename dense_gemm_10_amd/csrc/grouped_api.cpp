@@ -39,15 +39,31 @@ int64_t row_tiles(int64_t rows, int64_t groups, int64_t bm)
     return rows / bm + (groups < rows ? groups : rows);
 }
 
-// A grid of `a` x `b` workgroups of at most 1024 threads, if a launch can
-// have it.
-bool grid_ok(int64_t a, int64_t b, uint32_t *programs)
+// A grid of `a` x `b` workgroups of `threads` threads, if a launch can have
+// it: below 2^32 threads, with the 128 workgroups that launch_grouped_mixed
+// adds.  The kernels' 32-bit tile numbers are then far from their end.
+bool grid_ok(int64_t a, int64_t b, int32_t threads, uint32_t *programs)
 {
     int64_t p;
-    if (!mul_ok(a, b, &p) || p > (int64_t)UINT32_MAX / 1024)
+    if (!mul_ok(a, b, &p) || p > (int64_t)UINT32_MAX / threads - 128)
         return false;
     *programs = (uint32_t)p;
     return true;
+}
+
+// `chosen`, or where its grid is more than a launch can have the first of
+// `table` (tiles in ascending order) with larger tiles and a grid that is
+// not.  fits(k): k takes the problem and its grid can be launched; it sets
+// the plan's programs.
+template <typename K, size_t N, typename Fits>
+const K *fitting_kernel(const K *chosen, const K *const (&table)[N], Fits &&fits)
+{
+    if (fits(*chosen))
+        return chosen;
+    for (const K *k : table)
+        if (k->bm * k->bn > chosen->bm * chosen->bn && fits(*k))
+            return k;
+    return nullptr;
 }
 
 // ---- grouped products -------------------------------------------------------
@@ -121,11 +137,11 @@ dg_status validate(const dg_grouped_desc *d, Spans *s)
 
 using GroupedLaunch = hipError_t (*)(const GroupedArgs &, uint32_t, hipStream_t);
 
-// A kernel of the grouped products: its tile and its launchers (null: not
-// for this kind).
+// A kernel of the grouped products: its tile, the threads of a workgroup (at
+// most) and its launchers (null: not for this kind).
 struct GroupedKernel {
     const char *name;
-    int32_t bm, bn;
+    int32_t bm, bn, threads;
     GroupedLaunch ragged_m, ragged_k;
 };
 
@@ -149,20 +165,20 @@ hipError_t tile256_m(const GroupedArgs &a, uint32_t p, hipStream_t s)
                                  : launch_grouped16_m256_bf16(a, p, s);
 }
 
-const GroupedKernel kGeneric = {"generic", kGroupedGenericTile, kGroupedGenericTile, generic_m,
-                                generic_k};
-const GroupedKernel kTile256 = {"mfma16_256x256", 256, 256, tile256_m,
+const GroupedKernel kGeneric = {"generic", kGroupedGenericTile, kGroupedGenericTile, 256,
+                                generic_m, generic_k};
+const GroupedKernel kTile256 = {"mfma16_256x256", 256, 256, 256, tile256_m,
                                 launch_grouped16_k256};
-const GroupedKernel kTile128 = {"mfma16_128x128", 128, 128, launch_grouped16_m128,
+const GroupedKernel kTile128 = {"mfma16_128x128", 128, 128, 256, launch_grouped16_m128,
                                 launch_grouped16_k128};
-const GroupedKernel kTileF32 = {"mfma_f32_128x128", 128, 128, launch_grouped_f32_m,
+const GroupedKernel kTileF32 = {"mfma_f32_128x128", 128, 128, 256, launch_grouped_f32_m,
                                 launch_grouped_f32_k};
-const GroupedKernel kStream16x32 = {"stream_16x32", 16, 32, stream_m<0>, nullptr};
-const GroupedKernel kStream16x64 = {"stream_16x64", 16, 64, stream_m<1>, nullptr};
-const GroupedKernel kStream32x64 = {"stream_32x64", 32, 64, stream_m<2>, nullptr};
-const GroupedKernel *const kGrouped16[] = {&kTile256, &kTile128, &kStream16x32, &kStream16x64,
-                                           &kStream32x64};
-const GroupedKernel *const kGroupedF32[] = {&kTileF32, &kStream16x32, &kStream16x64, &kStream32x64};
+const GroupedKernel kStream16x32 = {"stream_16x32", 16, 32, 512, stream_m<0>, nullptr};
+const GroupedKernel kStream16x64 = {"stream_16x64", 16, 64, 512, stream_m<1>, nullptr};
+const GroupedKernel kStream32x64 = {"stream_32x64", 32, 64, 512, stream_m<2>, nullptr};
+const GroupedKernel *const kGrouped16[] = {&kStream16x32, &kStream16x64, &kStream32x64, &kTile128,
+                                           &kTile256};
+const GroupedKernel *const kGroupedF32[] = {&kStream16x32, &kStream16x64, &kStream32x64, &kTileF32};
 
 // The kernel of `table` that DG_FORCE_GROUPED names (benchmarking and
 // tests), or NULL.
@@ -250,16 +266,19 @@ const GroupedKernel *choose(const dg_grouped_desc *d, const void *A, const void 
 
 dg_status make_plan(const dg_grouped_desc *d, const void *A, const void *B, GroupedPlan *p)
 {
-    p->kernel = choose(d, A, B);
-    const int64_t bm = p->kernel->bm, bn = p->kernel->bn;
-    const int64_t tn = ceil_div(d->N, bn);
-    const int64_t tm = d->ragged == DG_RAGGED_K ? ceil_div(d->M, bm)
-                                                : row_tiles(d->rows, d->groups, bm);
-    int64_t t;
-    if (!mul_ok(tm, tn, &t) || t > INT32_MAX ||
-        !grid_ok(t, d->ragged == DG_RAGGED_K ? d->groups : 1, &p->programs))
-        return DG_ERROR_NOT_SUPPORTED;
-    return DG_SUCCESS;
+    const bool rk = d->ragged == DG_RAGGED_K;
+    auto fits = [&](const GroupedKernel &k) {
+        const int64_t tn = ceil_div(d->N, k.bn);
+        const int64_t tm = rk ? ceil_div(d->M, k.bm) : row_tiles(d->rows, d->groups, k.bm);
+        int64_t t;
+        return (rk ? k.ragged_k : k.ragged_m) && mul_ok(tm, tn, &t) && t <= INT32_MAX &&
+               grid_ok(t, rk ? d->groups : 1, k.threads, &p->programs);
+    };
+    const GroupedKernel *first = choose(d, A, B);
+    p->kernel = first == &kGeneric         ? (fits(kGeneric) ? &kGeneric : nullptr)
+                : d->a_type == DG_F32 ? fitting_kernel(first, kGroupedF32, fits)
+                                      : fitting_kernel(first, kGrouped16, fits);
+    return p->kernel ? DG_SUCCESS : DG_ERROR_NOT_SUPPORTED;
 }
 
 // ---- 4-bit weights ----------------------------------------------------------
@@ -327,10 +346,11 @@ const QweightKernel kQ32x32 = {"qstream_32x32", 32, 32, qrows<3>};
 const QweightKernel kQ32x64 = {"qstream_32x64", 32, 64, qrows<4>};
 const QweightKernel kQ32x128 = {"qstream_32x128", 32, 128, qrows<5>};
 const QweightKernel kQ64x256 = {"qtile_64x256", 64, 256, launch_qweight_tile};
-// group sizes that are multiples of 128 only; its choice has a rule of its own
+// group sizes that are multiples of 128 only
 const QweightKernel kQ64x512 = {"qtile_64x512", 64, 512, launch_qweight_wide_tile};
-const QweightKernel *const kQweight[] = {&kQ64x256, &kQ32x128, &kQ32x64, &kQ32x32,
-                                         &kQ16x64,  &kQ16x32,  &kQ16x16};
+const QweightKernel *const kQweight[] = {&kQ16x16, &kQ16x32,  &kQ16x64,  &kQ32x32,
+                                         &kQ32x64, &kQ32x128, &kQ64x256, &kQ64x512};
+constexpr int32_t kQweightThreads = 512;   // of the matrix-core kernels
 
 struct QweightPlan {
     const QweightKernel *kernel;
@@ -383,14 +403,12 @@ const QweightKernel *choose(const dg_qweight_desc *d, bool offsets, const void *
     if (!qstream_ok(d, offsets, A, Q))
         return &kQGeneric;
     const bool wide = d->group_size % 128 == 0;
-    const QweightKernel *const wide_only[] = {&kQ64x512};
-    if (const QweightKernel *k = wide ? forced_kernel(wide_only) : nullptr)
-        return k;
     if (const QweightKernel *k = forced_kernel(kQweight))
-        return k;
+        if (k != &kQ64x512 || wide)
+            return k;
     const int64_t rows = offsets ? d->M / d->groups : d->M;
     const int64_t want = rows <= 4 ? 512 : 256;
-    for (const QweightKernel *k : kQweight) {
+    for (const QweightKernel *k : {&kQ64x256, &kQ32x128, &kQ32x64, &kQ32x32, &kQ16x64, &kQ16x32}) {
         const bool rows_fit = k->bm == 64 ? rows >= 256 : k->bm == 32 ? rows > 16 : k->bm == 16;
         if (!rows_fit || ceil_div(d->N, k->bn) < ceil_div(want, row_tiles(d, offsets, *k)))
             continue;
@@ -404,10 +422,15 @@ const QweightKernel *choose(const dg_qweight_desc *d, bool offsets, const void *
 dg_status make_plan(const dg_qweight_desc *d, bool offsets, const void *A, const void *Q,
                     QweightPlan *p)
 {
-    p->kernel = choose(d, offsets, A, Q);
-    return grid_ok(row_tiles(d, offsets, *p->kernel), ceil_div(d->N, p->kernel->bn), &p->programs)
-               ? DG_SUCCESS
-               : DG_ERROR_NOT_SUPPORTED;
+    auto fits = [&](const QweightKernel &k) {
+        return (&k != &kQ64x512 || d->group_size % 128 == 0) &&
+               grid_ok(row_tiles(d, offsets, k), ceil_div(d->N, k.bn),
+                       &k == &kQGeneric ? 256 : kQweightThreads, &p->programs);
+    };
+    const QweightKernel *first = choose(d, offsets, A, Q);
+    p->kernel = first == &kQGeneric ? (fits(kQGeneric) ? &kQGeneric : nullptr)
+                                    : fitting_kernel(first, kQweight, fits);
+    return p->kernel ? DG_SUCCESS : DG_ERROR_NOT_SUPPORTED;
 }
 
 } // namespace

@@ -336,7 +336,10 @@ typedef struct dg_grouped_desc {
     const void *bias;
 } dg_grouped_desc;
 
-/* Enqueue the products on `stream`. */
+/* Enqueue the products on `stream`.  DG_ERROR_NOT_SUPPORTED also where even
+ * the largest tile makes a launch of 2^32 threads or more: with rows on 16
+ * bytes from about 2^24 tiles of 256 x 256 (16 bits) or 128 x 128 (fp32), else of
+ * 64 x 64; a group's last tile counts whole. */
 dg_status dg_gemm_grouped(const dg_grouped_desc *d, const void *A, const void *B, void *C,
                           const int32_t *offsets, void *stream);
 
@@ -387,7 +390,11 @@ typedef struct dg_qweight_desc {
     const void *bias;
 } dg_qweight_desc;
 
-/* Enqueue the product on `stream`.  Needs no workspace; may be captured. */
+/* Enqueue the product on `stream`.  Needs no workspace; may be captured.
+ * DG_ERROR_NOT_SUPPORTED also where even the largest tile makes a launch of
+ * 2^32 threads or more: from about 2^23 tiles of 64 x 256 (64 x 512 for group
+ * sizes that are multiples of 128), or 2^24 of 64 x 64 for operands off the
+ * 16-byte grid or K that is no multiple of 32. */
 dg_status dg_gemm_qweight(const dg_qweight_desc *d, const void *A, const void *Q,
                           const void *scales, const void *zeros, void *C,
                           const int32_t *offsets, void *stream);

@@ -178,3 +178,21 @@ def test_fp32_kernels_with_epilogues(kernel, order, monkeypatch):
         dg.gemm_grouped(Ad, W, _offsets(off), C, alpha=alpha, beta=beta, bias=b, act=act)
         check(C[inside], ref[inside], tol[inside], f"{alpha} {beta} {act}")
         assert torch.equal(C[~inside], C0[~inside])
+
+
+@pytest.mark.parametrize("N,kernel", [(2 ** 22, "stream_16x64"), (2 ** 23, "mfma16_128x128")])
+def test_grids_of_millions_of_workgroups(N, kernel):
+    """6.3 million workgroups, and a problem whose first choice would make
+    more threads than a launch can have."""
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    groups, rows, K = 64, 512, 32
+    A = torch.randint(-2, 3, (rows, K), generator=gen, device="cuda").bfloat16()
+    W = torch.randint(-2, 3, (N, K), generator=gen, device="cuda").bfloat16()
+    B = W.t().expand(groups, K, N)
+    off = sorted(torch.randint(0, rows + 1, (groups - 1,), generator=gen, device="cuda").tolist())
+    d = dg.make_grouped_desc("m", groups, rows, N, K=K, b_order="col", stride_b=0)
+    assert f"kernel={kernel} " in dg.dg_gemm_grouped_describe(d)
+    C = torch.full((rows, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    dg.gemm_grouped(A, B, _offsets([0] + off + [rows]), C)
+    for lo in range(0, N, 2 ** 21):                             # whole numbers below 2^8: exact in bf16
+        assert torch.equal(C[:, lo:lo + 2 ** 21].float(), A.float() @ W[lo:lo + 2 ** 21].float().t())

@@ -135,3 +135,21 @@ def test_infinities_and_large_values_follow_the_formula(kernel, g, dtype, expert
         [A[lo:hi].double() @ W[e].t() for e, (lo, hi) in enumerate(zip(off[:-1], off[1:]))])
     assert bool(ref[30, 12:299].isfinite().all()) and bool(ref[1].isinf().any()) and bool(ref[1].isnan().any())
     torch.testing.assert_close(C, ref, rtol=0, atol=0, equal_nan=True)
+
+
+def test_launch_past_the_first_choice():
+    """16 rows of so many columns that the 16 x 64 shape would make more
+    threads than a launch can have."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    M, N, K, g = 16, 2 ** 29, 32, 128
+    assert "kernel=qstream_32x128 " in dg.dg_gemm_qweight_describe(dg.make_qweight_desc(M, N, K, g))
+    A = torch.randint(-2, 3, (M, K), generator=gen, device="cuda").bfloat16()
+    Q = torch.randint(0, 256, (N, K // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    scales = torch.ones(N, 1, dtype=torch.bfloat16, device="cuda")
+    C = torch.full((M, N), float("nan"), dtype=torch.float16, device="cuda")
+    dg.gemm_qweight(A, Q, scales, None, C, group_size=g)
+    step = 2 ** 24
+    for lo in range(0, N, step):                                # whole numbers of at most 512: exact in fp16
+        q = Q[lo:lo + step]
+        w = torch.stack([q & 15, q >> 4], -1).flatten(-2).half() - 8
+        assert torch.equal(C[:, lo:lo + step].float(), A.float() @ w.float().t())
