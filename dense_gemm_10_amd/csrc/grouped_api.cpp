@@ -360,16 +360,17 @@ struct QweightPlan {
 // The matrix-core kernels read A and Q in whole 16-byte pieces and K in
 // whole steps of 32, and address a tile (up to 64 rows, 512 columns) with
 // 32-bit byte offsets.
-bool qstream_ok(const dg_qweight_desc *d, bool offsets, const void *A, const void *Q)
+bool qstream_ok(const dg_qweight_desc *d, const void *A, const void *Q)
 {
     return aligned_to(A, 16) && aligned_to(Q, 16) && d->lda % 8 == 0 && d->ldq % 16 == 0 &&
-           (!offsets || d->stride_q % 16 == 0) && d->K % 32 == 0 && d->lda < (1 << 24) &&
+           (d->groups <= 1 || d->stride_q % 16 == 0) && d->K % 32 == 0 && d->lda < (1 << 24) &&
            d->ldq < (1 << 23) && d->lds < (1 << 21);
 }
 
-int64_t row_tiles(const dg_qweight_desc *d, bool offsets, const QweightKernel &k)
+// One group's rows, with or without offsets, make at most ceil(M / bm) tiles.
+int64_t row_tiles(const dg_qweight_desc *d, const QweightKernel &k)
 {
-    return offsets ? row_tiles(d->M, d->groups, k.bm) : ceil_div(d->M, k.bm);
+    return d->groups > 1 ? row_tiles(d->M, d->groups, k.bm) : ceil_div(d->M, k.bm);
 }
 
 // Times a tile's place on the chip is taken: one workgroup per CU.
@@ -398,36 +399,35 @@ int64_t chip_passes(int64_t row_tiles, int64_t n, int64_t bn)
 //   64 rows, 16384 x 4096: 31.8 on 16 x 64, 31.6 on 32 x 32, 26.9 on 32 x 64
 //   512 rows, 4096 x 4096: 60.5 on 32 x 32, 44.9 on 32 x 64, 33 on 32 x
 //     128 (two column blocks per wavefront halve its reads of A from LDS)
-const QweightKernel *choose(const dg_qweight_desc *d, bool offsets, const void *A, const void *Q)
+const QweightKernel *choose(const dg_qweight_desc *d, const void *A, const void *Q)
 {
-    if (!qstream_ok(d, offsets, A, Q))
+    if (!qstream_ok(d, A, Q))
         return &kQGeneric;
     const bool wide = d->group_size % 128 == 0;
     if (const QweightKernel *k = forced_kernel(kQweight))
         if (k != &kQ64x512 || wide)
             return k;
-    const int64_t rows = offsets ? d->M / d->groups : d->M;
+    const int64_t rows = d->M / d->groups;
     const int64_t want = rows <= 4 ? 512 : 256;
     for (const QweightKernel *k : {&kQ64x256, &kQ32x128, &kQ32x64, &kQ32x32, &kQ16x64, &kQ16x32}) {
         const bool rows_fit = k->bm == 64 ? rows >= 256 : k->bm == 32 ? rows > 16 : k->bm == 16;
-        if (!rows_fit || ceil_div(d->N, k->bn) < ceil_div(want, row_tiles(d, offsets, *k)))
+        if (!rows_fit || ceil_div(d->N, k->bn) < ceil_div(want, row_tiles(d, *k)))
             continue;
-        const int64_t rt = row_tiles(d, offsets, *k);
+        const int64_t rt = row_tiles(d, *k);
         const bool fewer = 5 * chip_passes(rt, d->N, 512) < 3 * chip_passes(rt, d->N, 256);
         return k == &kQ64x256 && wide && fewer ? &kQ64x512 : k;
     }
     return &kQ16x16;
 }
 
-dg_status make_plan(const dg_qweight_desc *d, bool offsets, const void *A, const void *Q,
-                    QweightPlan *p)
+dg_status make_plan(const dg_qweight_desc *d, const void *A, const void *Q, QweightPlan *p)
 {
     auto fits = [&](const QweightKernel &k) {
         return (&k != &kQ64x512 || d->group_size % 128 == 0) &&
-               grid_ok(row_tiles(d, offsets, k), ceil_div(d->N, k.bn),
+               grid_ok(row_tiles(d, k), ceil_div(d->N, k.bn),
                        &k == &kQGeneric ? 256 : kQweightThreads, &p->programs);
     };
-    const QweightKernel *first = choose(d, offsets, A, Q);
+    const QweightKernel *first = choose(d, A, Q);
     p->kernel = first == &kQGeneric ? (fits(kQGeneric) ? &kQGeneric : nullptr)
                                     : fitting_kernel(first, kQweight, fits);
     return p->kernel ? DG_SUCCESS : DG_ERROR_NOT_SUPPORTED;
@@ -537,7 +537,7 @@ dg_status dg_gemm_qweight(const dg_qweight_desc *d, const void *A, const void *Q
         ranges_overlap(C, sp.c, d->bias, sp.bias) || ranges_overlap(C, sp.c, offsets, sp.offsets))
         return DG_ERROR_INVALID_VALUE;
     QweightPlan p;
-    st = make_plan(d, offsets != nullptr, A, Q, &p);
+    st = make_plan(d, A, Q, &p);
     if (st != DG_SUCCESS)
         return st;
     QweightArgs a;
@@ -586,7 +586,7 @@ dg_status dg_gemm_qweight_describe(const dg_qweight_desc *d, char *buf, size_t l
         return DG_SUCCESS;
     }
     QweightPlan p;
-    st = make_plan(d, d->groups > 1, nullptr, nullptr, &p);
+    st = make_plan(d, nullptr, nullptr, &p);
     if (st == DG_SUCCESS)
         snprintf(buf, len, "kernel=%s bm=%d bn=%d programs=%u", p.kernel->name, p.kernel->bm,
                  p.kernel->bn, p.programs);

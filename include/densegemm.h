@@ -399,8 +399,8 @@ dg_status dg_gemm_qweight(const dg_qweight_desc *d, const void *A, const void *Q
                           const void *scales, const void *zeros, void *C,
                           const int32_t *offsets, void *stream);
 
-/* One line on the kernel, tile and grid dg_gemm_qweight would run (operands
- * taken as aligned). */
+/* One line on the kernel, tile and grid dg_gemm_qweight would run, with or
+ * without offsets (operands taken as aligned). */
 dg_status dg_gemm_qweight_describe(const dg_qweight_desc *d, char *buf, size_t len);
 
 #ifdef __cplusplus

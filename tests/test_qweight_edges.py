@@ -153,3 +153,24 @@ def test_launch_past_the_first_choice():
         q = Q[lo:lo + step]
         w = torch.stack([q & 15, q >> 4], -1).flatten(-2).half() - 8
         assert torch.equal(C[:, lo:lo + step].float(), A.float() @ w.float().t())
+
+
+@pytest.mark.parametrize("M,N", [(1, 8320), (16, 9000), (32, 4100), (64, 4096), (300, 16600)])
+@pytest.mark.parametrize("stride", [0, 8])
+def test_one_group_with_offsets_runs_what_one_without_them_runs(M, N, stride):
+    """With one group the offsets change nothing in the kernel's choice, and
+    the distance of a second group, which is not there, neither: the same
+    sums, bit for bit, whatever the rows of the group."""
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    K, g = 1056, 32
+    A = torch.randn(M, K, generator=gen, device="cuda").bfloat16()
+    Q = torch.randint(0, 256, (N, K // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    scales = torch.rand(N, K // g, generator=gen, device="cuda")
+    one = Q.as_strided((1, N, K // 2), (N * K // 2 + stride, K // 2, 1))
+    ref = dg.gemm_qweight(A, Q, scales, group_size=g, out_dtype=torch.float32)
+    for lo, hi in ((0, M), (M // 3, M), (0, M - M // 4)):
+        C = torch.full((M, N), 3.0, device="cuda")
+        dg.gemm_qweight(A, one, scales[None], None, C, group_size=g,
+                        offsets=torch.tensor([lo, hi], dtype=torch.int32, device="cuda"))
+        assert bool((C[:lo] == 3.0).all()) and bool((C[hi:] == 3.0).all())
+        assert torch.equal(C[lo:hi], ref[lo:hi])
