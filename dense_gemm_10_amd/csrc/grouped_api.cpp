@@ -210,32 +210,36 @@ bool mfma_ok(const dg_grouped_desc *d, const void *A, const void *B)
 // The kernel for a problem.  Group lengths are unknown; the mean stands for
 // them, and half the groups are taken to end in one more tile.
 //
-// Ragged rows, by the mean rows of a group (us, MI355X, bf16):
+// Ragged rows, by the mean rows of a group (us, MI355X, bf16; ranges are of
+// boxes, orders of B, and weights in and out of the Infinity Cache):
 //   up to 8 rows, the 16-row streaming kernels: 64 groups, 512 rows, 2048 x
-//     2048: 98-100 against 98-118 on the 128 x 128 tile; 64 rows, 2048 x
-//     1024: 36 against 42-52.  32 columns per workgroup where 64 would make
-//     fewer than 512 workgroups (8 groups, 8 rows, 1024 x 1024: 5.5 against
-//     6.1-7.3);
-//   up to 16, the 32-row one: 1024 rows on those 64 groups 105 against
-//     112-120 on 16 rows, 4 groups, 64 rows, 4096 x 4096 31-34 against 43
-//     and 40-51 on the tile;
+//     2048: 98-101 against 98-118 on the 128 x 128 tile; 64 rows, 2048 x
+//     1024: 28-36 against 33-52.  32 columns per workgroup where 64 would
+//     make fewer than 512 workgroups (8 groups, 8 rows, 1024 x 1024: 3.6-5.5
+//     against 5.0-7.3);
+//   up to 16, the 32-row one: 1024 rows on those 64 groups 105-106 against
+//     112-120 on 16 rows (and 102-115 on the tile), 4 groups, 64 rows, 4096 x
+//     4096 25-34 against 32-43 and 29-51 on the tile;
 //   fp32 keeps the 32-row one below 1024 tiles of 128 x 128 (1000 rows, 5
-//     groups, 512 x 260: 10 against 63; 4096 rows, 16 groups, 2048 x 2048:
-//     332-390 against 393-407) and takes the tile above (8192 rows, 2048 x
-//     4096: 1151-1166 against 1228-1440);
+//     groups, 512 x 260: 9.2 against 62, and 8.8 and 10.5 on 16 rows x 32 and
+//     64; 4096 rows, 16 groups, 2048 x 2048: 327-390 against 393-407, and
+//     482 and 342 on 16 rows) and takes the tile above (8192 rows, 2048 x
+//     4096: 1151-1166, on another box 1280, against 1228-1440);
 //   above, 16 bits, a tile: 256 x 256 (with half-height tiles, see
 //     grouped16.hpp) for groups of 128 rows and more, K from 768 and at
 //     least 128 tiles, else 128 x 128 (8192 rows, 16 groups, 4096 x 4096:
-//     305-313 against 390-418; 2000 rows, 16 groups, 4096 x 2048: 78 against
-//     103; but 1000 rows, 4 groups, 4096 x 1024, 28 tiles: 61-73 against
-//     49-51, and 6000 rows, 48 groups, 512 x 1024: 32 against 27).
+//     305-316 against 390-418; 2000 rows, 16 groups, 4096 x 2048: 75-78
+//     against 101-103; but 1000 rows, 4 groups, 4096 x 1024, 28 tiles: 61-74
+//     against 33-51, and 6000 rows, 48 groups, 512 x 1024: 27-32 against
+//     22-27).
 // Ragged K: the 128 x 128 tile, whose other workgroups on a CU cover one's
-// epilogue (16 groups of 2048 x 2048, 8192 rows: 102 against 112; 32 of 512
-// x 1024: 24 against 29), unless the groups are long and 256 x 256 tiles fill
-// the chip twice, so that long and short groups even out (16384 rows, 8
-// groups, 4096 x 4096: 505 against 585, 2048 x 2048: 167 against 185; but
-// 8192 rows, 1024 x 2048, 256 tiles: 58 against 52), or once with one group
-// (4096 rows, 4096 x 4096: 120 against 133).
+// epilogue (16 groups of 2048 x 2048, 8192 rows: 99-102 against 100-112; 32
+// of 512 x 1024: 22-24 against 24-29), unless the groups are long and 256 x
+// 256 tiles fill the chip twice, so that long and short groups even out
+// (16384 rows, 8 groups, 4096 x 4096: 484-505 against 521-585, 2048 x 2048:
+// 136-167 against 142-185; but 8192 rows, 1024 x 2048, 256 tiles: 52-58
+// against 45-52), or once with one group (4096 rows, 4096 x 4096: 112-120
+// against 123-133).
 const GroupedKernel *choose(const dg_grouped_desc *d, const void *A, const void *B)
 {
     if (!mfma_ok(d, A, B))
@@ -383,22 +387,26 @@ int64_t chip_passes(int64_t row_tiles, int64_t n, int64_t bn)
 }
 
 // From 256 rows a group, if 64 x 256 tiles fill the chip, the tile (us, 4096
-// x 4096, bf16, group size 128): 1024 rows 48 against 62, 2048 rows 95
-// against 120; 256 rows of 14336 x 4096 49 against 64; where they do not, it
-// loses (256 rows of 4096 x 4096: 46 against 23).  A pass of 64 x 512 tiles
-// over the chip takes 78-84 us where one of 64 x 256 takes 47 (four column
-// blocks per wavefront read a row of A once, but hold 256 registers), so they
-// are taken where they need less than 3/5 of the passes: 2048 rows 84 against
-// 95, 8192 x 8192 311 against 344; 1024 rows 78 against 48.
+// x 4096, bf16, group size 128): 1024 rows 49 against 63 on 32 x 128, 2048
+// rows 97 against 124; 256 rows of 16384 x 4096 49 against 63 (of 14336 x
+// 4096, 224 tiles, which the rule leaves to 32 x 128, 48 against 60); where
+// they do not, it loses (256 rows of 4096 x 4096: 46 against 21).  A pass of
+// 64 x 512 tiles over the chip takes 79-86 us where one of 64 x 256 takes
+// 46-49 (four column blocks per wavefront read a row of A once, but hold 256
+// registers), so they are taken where they need less than 3/5 of the passes:
+// 2048 rows 86 against 97, of 8192 x 8192 329 against 365; 1024 rows 81
+// against 49.
 // Else 32 rows where a group has more than 16, and the widest workgroup
 // (each reads A once) that still makes 512 of them for up to 4 rows, 256
 // for more, where A's traffic counts:
 //   1 row,   4096 x 4096: 5.4 on 16 columns, 6.9 on 32, 10.4 on 64;
 //            16384 x 4096: 12.5, 10.2, 11.8;  8192 x 8192: 10.5, 12.6, 19.1
-//   16 rows, 4096 x 4096: 7.2, 9.2, 11.8;  16384 x 4096: 18.6, 14.0, 13.3
-//   64 rows, 16384 x 4096: 31.8 on 16 x 64, 31.6 on 32 x 32, 26.9 on 32 x 64
-//   512 rows, 4096 x 4096: 60.5 on 32 x 32, 44.9 on 32 x 64, 33 on 32 x
-//     128 (two column blocks per wavefront halve its reads of A from LDS)
+//   16 rows, 4096 x 4096: 6.1-7.2, 7.8-9.2, 11.1-11.8;  16384 x 4096:
+//     15.9-18.6, 11.6-14.0, 12.0-13.3
+//   64 rows, 16384 x 4096: 30 on 16 x 64, 30 on 32 x 32, 25 on 32 x 64, 21 on
+//     32 x 128
+//   512 rows, 4096 x 4096: 55 on 32 x 32, 45 on 32 x 64, 33 on 32 x 128 (two
+//     column blocks per wavefront halve its reads of A from LDS)
 const QweightKernel *choose(const dg_qweight_desc *d, const void *A, const void *Q)
 {
     if (!qstream_ok(d, A, Q))

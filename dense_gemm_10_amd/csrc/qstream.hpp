@@ -17,9 +17,9 @@
 // output whose sums are not finite is formed again (defined_product).
 //
 // Measured (MI355X): one row through 16384 x 8192 (fp16, groups of 64) 17.4
-// us, 4.2 TB/s, bound by the codes' bytes; through 4096 x 4096 5.4 us in a
+// us, 4.2 TB/s, bound by the codes' bytes; through 4096 x 4096 5.1 us in a
 // replayed graph, 7.4 us called from the host, bound by launch and latency;
-// 2048 rows through 4096 x 4096 (bf16, groups of 128) 84 us, 0.82 PFLOP/s,
+// 2048 rows through 4096 x 4096 (bf16, groups of 128) 84-86 us, 0.8 PFLOP/s,
 // bound by the panel's chain of stage, barrier and first operand reads, which
 // two wavefronts per SIMD do not cover.
 //

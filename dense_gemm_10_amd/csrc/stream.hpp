@@ -1,7 +1,7 @@
 // Products of few rows of A with a large B: each weight is used once or a
 // few times, so the kernels are bound by reading B from memory.  Shared by
-// the grouped products (kernel_stream.hip) and the
-// products with 4-bit weights (kernel_qstream.hip).
+// the grouped products (kernel_stream.hip) and the products with 4-bit
+// weights (kernel_qstream.hip, kernel_qtile.hip).
 //
 // A workgroup owns 16 FM rows x 16 FN columns of one group's output and its
 // KW wavefronts take the steps along K in turn (wavefront w: steps w, w +
@@ -15,7 +15,10 @@
 //
 // Measured (MI355X): 64 rows on 64 groups, 2048 x 1024 bf16 36.4 us, 171 MB
 // at 4.7 TB/s, what a large copy reaches; 1000 rows, 5 groups, 512 x 260
-// fp32 9.7 us, bound by launch and by the latency of its few steps.
+// fp32 9.2 us in a replayed graph (a fill of 64 floats there: 1.7): at most
+// 180 workgroups, so that 76 of the 256 compute units idle, and each has 2.1
+// MFLOP, 3.4 us of a unit's fp32 matrix rate; the rest is start, the latency
+// of the few steps and the epilogue.
 #pragma once
 #include "grouped.hpp"
 #include "mfma16.hpp"
