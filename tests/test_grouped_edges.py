@@ -196,3 +196,35 @@ def test_grids_of_millions_of_workgroups(N, kernel):
     dg.gemm_grouped(A, B, _offsets([0] + off + [rows]), C)
     for lo in range(0, N, 2 ** 21):                             # whole numbers below 2^8: exact in bf16
         assert torch.equal(C[:, lo:lo + 2 ** 21].float(), A.float() @ W[lo:lo + 2 ** 21].float().t())
+
+
+def _most_groups(gen, rows, groups=65536):
+    """Offsets of 65536 groups of no, one or a few rows, and each row's group."""
+    count = torch.bincount(torch.randint(0, groups, (rows,), generator=gen, device="cuda"), minlength=groups)
+    count[1000:1200], count[-1] = 0, 40
+    count[40000] += rows - 7 - int(count.sum())                 # seven rows behind the last group
+    off = torch.cat([torch.zeros(1, dtype=torch.int64, device="cuda"), count.cumsum(0)])
+    return off.int(), torch.repeat_interleave(torch.arange(groups, device="cuda"), count)
+
+
+@pytest.mark.parametrize("kernel", ["", "mfma16_128x128", "mfma16_256x256"])
+def test_the_most_groups(kernel, monkeypatch):
+    if kernel:
+        monkeypatch.setenv("DG_FORCE_GROUPED", kernel)
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    groups, rows, K, N, M = 65536, 70000, 32, 24, 16
+    off, of_row = _most_groups(gen, rows)
+
+    def ints_on(*shape):
+        return torch.randint(-2, 3, shape, generator=gen, device="cuda").bfloat16()
+
+    A, B, G = ints_on(rows, K), ints_on(groups, K, N), ints_on(rows, N)
+    C = torch.full((rows, N), 9.0, device="cuda")
+    dg.gemm_grouped(A, B, off, C)
+    n = of_row.numel()
+    assert n == rows - 7 and bool((C[n:] == 9.0).all())
+    assert torch.equal(C[:n], torch.bmm(A[:n, None].float(), B[of_row].float())[:, 0])
+    got = dg.gemm_grouped_k(A[:, :M].t(), G, off, out_dtype=torch.float32)
+    ref = torch.zeros(groups, M, N, device="cuda")
+    ref.index_add_(0, of_row, A[:n, :M, None].float() * G[:n, None].float())
+    assert torch.equal(got, ref)

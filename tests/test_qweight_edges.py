@@ -174,3 +174,24 @@ def test_one_group_with_offsets_runs_what_one_without_them_runs(M, N, stride):
                         offsets=torch.tensor([lo, hi], dtype=torch.int32, device="cuda"))
         assert bool((C[:lo] == 3.0).all()) and bool((C[hi:] == 3.0).all())
         assert torch.equal(C[lo:hi], ref[lo:hi])
+
+
+@pytest.mark.parametrize("kernel", ["", "qstream_16x16", "qstream_32x128"])
+def test_the_most_groups(kernel, monkeypatch):
+    if kernel:
+        monkeypatch.setenv("DG_FORCE_GROUPED", kernel)
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    groups, rows, N, K, g = 65536, 70000, 24, 32, 32
+    count = torch.bincount(torch.randint(0, groups, (rows - 50,), generator=gen, device="cuda"), minlength=groups)
+    count[-1] += 43                                             # seven rows behind the last group
+    off = torch.cat([torch.zeros(1, dtype=torch.int64, device="cuda"), count.cumsum(0)]).int()
+    of_row = torch.repeat_interleave(torch.arange(groups, device="cuda"), count)
+    A = torch.randint(-2, 3, (rows, K), generator=gen, device="cuda").bfloat16()
+    Q = torch.randint(0, 256, (groups, N, K // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    scales = 2.0 ** torch.randint(-1, 2, (groups, N, 1), generator=gen, device="cuda").float()
+    C = torch.full((rows, N), 9.0, device="cuda")
+    dg.gemm_qweight(A, Q, scales, None, C, group_size=g, offsets=off)
+    n = of_row.numel()
+    assert n == rows - 7 and bool((C[n:] == 9.0).all())
+    w = (torch.stack([Q & 15, Q >> 4], -1).flatten(-2).float() - 8) * scales
+    assert torch.equal(C[:n], torch.bmm(w[of_row], A[:n, :, None].float())[:, :, 0])
