@@ -210,8 +210,8 @@ bool mfma_ok(const dg_grouped_desc *d, const void *A, const void *B)
 // The kernel for a problem.  Group lengths are unknown; the mean stands for
 // them, and half the groups are taken to end in one more tile.
 //
-// Ragged rows, by the mean rows of a group (us, MI355X, bf16; ranges are of
-// boxes, orders of B, and weights in and out of the Infinity Cache):
+// Ragged rows, by the mean rows of a group (us, MI355X, bf16; ranges span
+// cards, orders of B, and weights in and out of the Infinity Cache):
 //   up to 8 rows, the 16-row streaming kernels: 64 groups, 512 rows, 2048 x
 //     2048: 98-101 against 98-118 on the 128 x 128 tile; 64 rows, 2048 x
 //     1024: 28-36 against 33-52.  32 columns per workgroup where 64 would
@@ -224,7 +224,7 @@ bool mfma_ok(const dg_grouped_desc *d, const void *A, const void *B)
 //     groups, 512 x 260: 9.2 against 62, and 8.8 and 10.5 on 16 rows x 32 and
 //     64; 4096 rows, 16 groups, 2048 x 2048: 327-390 against 393-407, and
 //     482 and 342 on 16 rows) and takes the tile above (8192 rows, 2048 x
-//     4096: 1151-1166, on another box 1280, against 1228-1440);
+//     4096: 1151-1166, on another card 1280, against 1228-1440);
 //   above, 16 bits, a tile: 256 x 256 (with half-height tiles, see
 //     grouped16.hpp) for groups of 128 rows and more, K from 768 and at
 //     least 128 tiles, else 128 x 128 (8192 rows, 16 groups, 4096 x 4096:
@@ -279,9 +279,12 @@ dg_status make_plan(const dg_grouped_desc *d, const void *A, const void *B, Grou
                grid_ok(t, rk ? d->groups : 1, k.threads, &p->programs);
     };
     const GroupedKernel *first = choose(d, A, B);
-    p->kernel = first == &kGeneric         ? (fits(kGeneric) ? &kGeneric : nullptr)
-                : d->a_type == DG_F32 ? fitting_kernel(first, kGroupedF32, fits)
-                                      : fitting_kernel(first, kGrouped16, fits);
+    if (first == &kGeneric)
+        p->kernel = fits(kGeneric) ? &kGeneric : nullptr;
+    else if (d->a_type == DG_F32)
+        p->kernel = fitting_kernel(first, kGroupedF32, fits);
+    else
+        p->kernel = fitting_kernel(first, kGrouped16, fits);
     return p->kernel ? DG_SUCCESS : DG_ERROR_NOT_SUPPORTED;
 }
 
@@ -436,8 +439,10 @@ dg_status make_plan(const dg_qweight_desc *d, const void *A, const void *Q, Qwei
                        &k == &kQGeneric ? 256 : kQweightThreads, &p->programs);
     };
     const QweightKernel *first = choose(d, A, Q);
-    p->kernel = first == &kQGeneric ? (fits(kQGeneric) ? &kQGeneric : nullptr)
-                                    : fitting_kernel(first, kQweight, fits);
+    if (first == &kQGeneric)
+        p->kernel = fits(kQGeneric) ? &kQGeneric : nullptr;
+    else
+        p->kernel = fitting_kernel(first, kQweight, fits);
     return p->kernel ? DG_SUCCESS : DG_ERROR_NOT_SUPPORTED;
 }
 
