@@ -215,7 +215,7 @@ def _own(s):
         if s["grad"]:
             return (y, *dg.combine_tokens_grad(s["dy"], s["z"], s["place"], s["w"], dz=s["dz"]))
         return y
-    return dg.gemm_i8(s["x"], s["B"], None, s["t"], s["C"], offsets=s.get("offsets"), bias=s["bias_v"], act=s["act"])
+    return dg.gemm_scaled(s["x"], s["B"], None, s["t"], s["C"], offsets=s.get("offsets"), bias=s["bias_v"], act=s["act"])
 
 
 def _act(v, act):
