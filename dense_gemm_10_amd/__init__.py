@@ -295,3 +295,7 @@ from .grouped import (  # noqa: E402  (uses the names above)
     DG_RAGGED_K, DG_RAGGED_M, DgGroupedDesc, DgQweightDesc, dg_gemm_grouped,
     dg_gemm_grouped_describe, dg_gemm_qweight, dg_gemm_qweight_describe, gemm_grouped,
     gemm_grouped_k, gemm_qweight, make_grouped_desc, make_qweight_desc)
+from .tokens import (  # noqa: E402
+    DgCombineDesc, DgDispatchDesc, DgQuantizeDesc, combine_tokens, combine_tokens_grad, dg_combine,
+    dg_combine_grad, dg_dispatch, dg_quantize, dg_spread, dispatch_tokens, make_combine_desc,
+    make_dispatch_desc, make_quantize_desc, quantize_rows, sort_tokens, spread_tokens)

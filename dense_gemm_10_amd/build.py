@@ -58,6 +58,10 @@ SOURCES = [
     "kernel_stream.hip",
     "kernel_qstream.hip",
     "kernel_qtile.hip",
+    "tokens_api.cpp",
+    "kernel_dispatch.hip",
+    "kernel_combine.hip",
+    "kernel_quantize.hip",
 ]
 
 

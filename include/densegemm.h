@@ -403,6 +403,117 @@ dg_status dg_gemm_qweight(const dg_qweight_desc *d, const void *A, const void *Q
  * without offsets (operands taken as aligned). */
 dg_status dg_gemm_qweight_describe(const dg_qweight_desc *d, char *buf, size_t len);
 
+/* ---- tokens sorted by group, and back -----------------------------------------
+ *
+ * A router names top_k groups (experts) for every token.  Slot s = t * top_k
+ * + j is token t's j-th choice, S = tokens * top_k slots in all, and
+ * index[t][j] its group; a value outside [0, groups) names no group (padding
+ * tokens, choices over an expert's capacity).  dg_dispatch sorts the slots
+ * by group, those of one group in ascending order, and writes
+ *
+ *   offsets  groups + 1 int32, as dg_gemm_grouped reads them: group e is
+ *            rows [offsets[e], offsets[e + 1]); offsets[0] = 0;
+ *   order    S int32: the slot of every row, -1 from row offsets[groups] on;
+ *   place    tokens x top_k int32, packed: the row of every slot, -1 for a
+ *            slot of no group (so order[place[s]] == s);
+ *   rows     S x width: row place[t][j] is x[t].  Rows from offsets[groups]
+ *            on are left as they were.
+ *
+ * x and rows NULL: only the maps.  dg_spread writes the rows alone, from a
+ * given place:  rows[place[t][j]] = x[t].
+ *
+ * dg_combine brings rows back:
+ *
+ *     y[t] = sum_j weights[t][j] * z[place[t][j]] + beta * y[t]
+ *
+ * over the slots with a row, in the order of j, in fp32, rounded once;
+ * weights NULL: ones, which with z = the rows' gradients is the gradient of
+ * dg_dispatch and dg_spread.  dg_combine_grad is its own gradient: for every
+ * slot with a row
+ *
+ *     dz[place[t][j]] = weights[t][j] * dy[t]
+ *     dweights[t][j]  = sum_c dy[t][c] * z[place[t][j]][c]
+ *
+ * and dweights 0 for a slot without; rows of dz that no slot has are left as
+ * they were.  A place outside [0, rows) is one without a row, so no content
+ * of the arrays makes a call read or write outside its operands.  Two slots
+ * may have one row in dg_combine; in dg_spread and dg_combine_grad what that
+ * row then gets is one of the two.
+ *
+ * Types, ownership, streams and errors as in dg_gemm; no workspace, nothing
+ * allocated, nothing read back; calls may be captured into HIP graphs.
+ *
+ * All integer fields are in ELEMENTS.
+ *   struct_size   sizeof(dg_dispatch_desc), sizeof(dg_combine_desc).
+ *   x_type        of x and rows (any dg_dtype).
+ *   index_bits    32 or 64: signed integers.
+ *   tokens, top_k, rows   >= 0, tokens * top_k and rows at most 2^31 - 1.
+ *   groups        0 .. 8192 (more: DG_ERROR_NOT_SUPPORTED).
+ *   rows          dg_spread: allocated rows of `rows`; dg_combine and
+ *                 dg_combine_grad: of z and dz.  dg_dispatch ignores it:
+ *                 `rows` has S.
+ *   ld_index, ldx, ldr, ldz, lddz, ldy, ldw   leading dimensions of index,
+ *                 x, rows, z, dz, y (or dy) and weights; each >= max(1, the
+ *                 row's length).  place and dweights are packed.
+ *   z_type, y_type   of z and dz, and of y or dy: the same, or y_type F32.
+ *   w_type        of weights and dweights (any dg_dtype). */
+typedef struct dg_dispatch_desc {
+    uint32_t struct_size;
+    int32_t x_type;
+    int32_t index_bits;
+    int64_t tokens, top_k, groups, rows, width;
+    int64_t ld_index, ldx, ldr;
+} dg_dispatch_desc;
+
+typedef struct dg_combine_desc {
+    uint32_t struct_size;
+    int32_t z_type, y_type, w_type;
+    int64_t tokens, top_k, rows, width;
+    int64_t ldz, lddz, ldy, ldw;
+    float beta;
+} dg_combine_desc;
+
+dg_status dg_dispatch(const dg_dispatch_desc *d, const void *index, const void *x,
+                      int32_t *offsets, int32_t *order, int32_t *place, void *rows,
+                      void *stream);
+
+dg_status dg_spread(const dg_dispatch_desc *d, const int32_t *place, const void *x, void *rows,
+                    void *stream);
+
+dg_status dg_combine(const dg_combine_desc *d, const void *z, const int32_t *place,
+                     const void *weights, void *y, void *stream);
+
+/* dz or dweights may be NULL (not wanted); z is read for dweights only.  beta
+ * is ignored.  weights NULL: ones. */
+dg_status dg_combine_grad(const dg_combine_desc *d, const void *dy, const void *z,
+                          const int32_t *place, const void *weights, void *dz, void *dweights,
+                          void *stream);
+
+/* ---- products in 8-bit integers -------------------------------------------------
+ *
+ * dg_quantize makes 8-bit codes of every row of x, and its scale:
+ *
+ *     scales[t] = max_k |x[t][k]| / 127         (fp32)
+ *     q[t][k]   = 127 * x[t][k] / max, to the nearest integer, ties to even
+ *
+ * the codes from the exact quotient; a row of zeros gets scale 0 and codes 0,
+ * a row that holds an infinity or NaN gets scale NaN and codes 0.  With
+ * `place` (tokens x top_k int32, packed, as dg_dispatch writes it) the codes
+ * and scale of token t go to the rows place[t][j] of q and scales, in
+ * [0, rows); other rows are left as they were.  place NULL: row t, and rows
+ * and top_k are ignored.
+ *   x_type any dg_dtype; ldx, ldq >= max(1, width); tokens * top_k and rows
+ *   at most 2^31 - 1. */
+typedef struct dg_quantize_desc {
+    uint32_t struct_size;
+    int32_t x_type;
+    int64_t tokens, top_k, rows, width;
+    int64_t ldx, ldq;
+} dg_quantize_desc;
+
+dg_status dg_quantize(const dg_quantize_desc *d, const void *x, const int32_t *place, int8_t *q,
+                      float *scales, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
