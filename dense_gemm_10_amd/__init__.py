@@ -299,3 +299,6 @@ from .tokens import (  # noqa: E402
     DgCombineDesc, DgDispatchDesc, DgQuantizeDesc, combine_tokens, combine_tokens_grad, dg_combine,
     dg_combine_grad, dg_dispatch, dg_quantize, dg_spread, dispatch_tokens, make_combine_desc,
     make_dispatch_desc, make_quantize_desc, quantize_rows, sort_tokens, spread_tokens)
+from .scaled import (  # noqa: E402
+    DG_I8, DgScaledDesc, dg_gemm_scaled, dg_gemm_scaled_describe, dg_gemm_scaled_workspace_size, gemm_scaled,
+    make_scaled_desc)

@@ -62,6 +62,9 @@ SOURCES = [
     "kernel_dispatch.hip",
     "kernel_combine.hip",
     "kernel_quantize.hip",
+    "scaled_api.cpp",
+    "kernel_scaled_stream.hip",
+    "kernel_scaled_tile.hip",
 ]
 
 

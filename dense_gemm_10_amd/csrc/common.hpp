@@ -40,7 +40,7 @@ struct GemmArgs {
 
 enum { ACT_NONE = 0, ACT_GELU_ERF = 1, ACT_GELU_TANH = 2 };
 // element types, numbered as dg_dtype
-enum { DT_F32 = 0, DT_BF16 = 1, DT_F16 = 2 };
+enum { DT_F32 = 0, DT_BF16 = 1, DT_F16 = 2, DT_I8 = 3 };
 
 // ---- 16-bit floats <-> fp32 -----------------------------------------------
 __device__ __forceinline__ float bf16_to_f32(uint16_t h)

@@ -18,6 +18,9 @@
 // registers, 32 x 32 x 16 MFMA fragments).  The multi-stage ring below is
 // the double buffering of that page's section 2.8 taken further.
 //
+// 8-bit integers (T = DT_I8, the products of kernel_scaled_tile.hip) run on
+// the same bytes: sizes, leading dimensions and K are then in pairs of them.
+//
 // Operands: an MFMA lane consumes 8 consecutive k of row (l mod 32) of A
 // and of column (l mod 32) of B.  A row-major (M x K) and B column-major
 // (K x N) have K contiguous and are staged as rows of K (below); a
@@ -79,6 +82,8 @@ typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 // Fragment type of element type T, and the 32 x 32 x 16 MFMA on it.
 template <int T> struct frag_of { using type = bf16x8_t; };
 template <> struct frag_of<DT_F16> { using type = f16x8_t; };
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+template <> struct frag_of<DT_I8> { using type = i32x4_t; };     // 16 of them
 
 __device__ __forceinline__ f32x16_t mfma_32x32x16(bf16x8_t a, bf16x8_t b, f32x16_t c)
 {
@@ -106,15 +111,35 @@ __device__ __forceinline__ f32x4_t mfma_16x16x32(f16x8_t a, f16x8_t b, f32x4_t c
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
+// 8-bit integers: 16 x 16 x 64 with the lanes of the 16 x 16 x 32 shape, 16
+// bytes of a row per lane, so that a row of 2 k 8-bit integers is loaded,
+// staged and fed exactly as one of k 16-bit elements.
+__device__ __forceinline__ i32x4_t mfma_16x16x64(i32x4_t a, i32x4_t b, i32x4_t c)
+{
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+}
+
 // Accumulators of one MFMA block: 32 x 32 (16 per lane) or 16 x 16 (4).
-template <int MS> struct acc_of { using type = f32x16_t; };
-template <> struct acc_of<16> { using type = f32x4_t; };
+template <int MS, int T = DT_BF16> struct acc_of { using type = f32x16_t; };
+template <int T> struct acc_of<16, T> { using type = f32x4_t; };
+template <> struct acc_of<16, DT_I8> { using type = i32x4_t; };
 
 template <typename F>
 __device__ __forceinline__ f32x16_t mfma_block(F a, F b, f32x16_t c) { return mfma_32x32x16(a, b, c); }
 template <typename F>
 __device__ __forceinline__ f32x4_t mfma_block(F a, F b, f32x4_t c) { return mfma_16x16x32(a, b, c); }
+__device__ __forceinline__ i32x4_t mfma_block(i32x4_t a, i32x4_t b, i32x4_t c)
+{
+    return mfma_16x16x64(a, b, c);
+}
 
+// What the sums of an 8-bit product are multiplied by: a scale for each row
+// and each column of the tile's matrix (null: ones).
+struct RowColScales {
+    const float *rows;
+    const void *cols;
+    int32_t cols_type;
+};
 
 
 // s_waitcnt immediate: wait until at most n vector-memory loads of this
@@ -317,7 +342,8 @@ __device__ __forceinline__ frag_t tr_fragment(uint32_t addr0)
 template <int T, int BM, int BN, int WM, int WN, int kStages, int MBK, bool AT, bool BT,
           int MS = 32>
 __device__ __forceinline__ void mfma16_tile(const GemmArgs &g, TileCoord tc, int64_t kb,
-                                            int64_t ke, float *part, uint4 *lds)
+                                            int64_t ke, float *part, uint4 *lds,
+                                            const RowColScales &scales = {})
 {
     using frag_t = typename frag_of<T>::type;
     constexpr int NT = 64 * WM * WN;
@@ -328,9 +354,10 @@ __device__ __forceinline__ void mfma16_tile(const GemmArgs &g, TileCoord tc, int
     constexpr int CPS = KD / 8;                  // 16-byte chunks of a fragment row per k-step
     constexpr int CPR = MBK / 8;                 // 16-byte chunks per stage row
     constexpr int KS = MBK / KD;                 // MFMA k-steps per stage
-    using acc_t = typename acc_of<MS>::type;
+    using acc_t = typename acc_of<MS, T>::type;
     constexpr int NV = MS == 32 ? 16 : 4;        // accumulators per lane per block
     static_assert(MS == 32 || MS == 16, "MFMA block size");
+    static_assert(T != DT_I8 || (MS == 16 && !AT && !BT), "8-bit operands: rows of K");
     constexpr int RPI = 64 / CPR;                // stage rows per DMA instruction
     constexpr int ROWS = BM + BN;                // stage rows: A rows, then B columns
     constexpr int GROUPS = ROWS / RPI;           // DMA instructions per stage
@@ -665,6 +692,29 @@ __device__ __forceinline__ void mfma16_tile(const GemmArgs &g, TileCoord tc, int
                 g, (char *)part, BN, BM, BN, n0, (float *)lds, acc);
         else
             tile_epilogue<BM, BN, WM, WN, REGS>(g, tc, (float *)lds, m0, n0, acc);
+    } else if constexpr (T == DT_I8) {
+        // the exact sums to fp32, times the scales of their row and column
+        f32x4_t f[FM][FN];
+        float sc[FN];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const int64_t c = wn * TN + MS * j + frag_row;
+            sc[j] = scales.cols ? load_as_f32(scales.cols, scales.cols_type, n0 + (c < b_ext ? c : b_ext - 1))
+                                : 1.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int64_t r = wm * TM + MS * i + 4 * frag_grp + v;
+                const float sr = scales.rows ? scales.rows[m0 + (r < a_ext ? r : a_ext - 1)] : 1.0f;
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+                    f[i][j][v] = (float)acc[i][j][v] * sr * sc[j];
+            }
+        }
+        const Acc16View<FM, FN> view{f};
+        tile_epilogue<BM, BN, WM, WN, REGS>(g, tc, (float *)lds, m0, n0, view);
     } else {
         const Acc16View<FM, FN> view{acc};
         if (part)

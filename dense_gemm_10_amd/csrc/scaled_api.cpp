@@ -1,0 +1,277 @@
+// C ABI of the products in 8-bit integers: host-side validation (no HIP
+// calls), choice of the kernel and launch.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+#include <stdio.h>
+#include <stdlib.h>
+#include <string.h>
+
+#include "../../include/densegemm.h"
+#include "checks.hpp"
+#include "scaled.hpp"
+#include "tokens.hpp"
+
+using namespace dg;
+
+namespace {
+
+constexpr int64_t kMaxGroups = 65536;
+constexpr int64_t kMaxK = 131071;        // 2^14 each: below 2^31
+
+bool float_type(int32_t t) { return t == DG_F32 || t == DG_BF16 || t == DG_F16; }
+
+int64_t a_bytes(const dg_scaled_desc *d) { return d->a_type == DG_I8 ? 1 : elem_size(d->a_type); }
+
+// Bytes of `count` matrices of `rows` rows of `len` elements, `ld` apart,
+// `stride` from one matrix to the next.
+bool bytes_of(int64_t count, int64_t stride, int64_t rows, int64_t len, int64_t ld, int64_t es,
+              int64_t *bytes)
+{
+    int64_t span, total;
+    return matrix_span(DG_ROW_MAJOR, rows, len, ld, &span) &&
+           batch_span(span, count, stride, &total) && mul_ok(total, es, bytes);
+}
+
+struct Spans {
+    int64_t a, sa, b, sb, c, bias, offsets;      // bytes
+    int64_t codes, workspace;                    // of a float A
+};
+
+bool is_noop(const dg_scaled_desc *d) { return d->groups == 0 || d->N == 0 || d->M == 0; }
+bool reads_ab(const dg_scaled_desc *d) { return d->alpha != 0.0f && d->K > 0; }
+
+// Leading dimension of the codes made of a float A: rows on 16 bytes.
+int64_t codes_ld(const dg_scaled_desc *d) { return d->K > 0 ? ceil_div(d->K, 16) * 16 : 16; }
+
+dg_status validate(const dg_scaled_desc *d, Spans *s)
+{
+    if (!d || d->struct_size != sizeof(dg_scaled_desc))
+        return DG_ERROR_INVALID_VALUE;
+    if ((!float_type(d->a_type) && d->a_type != DG_I8) || !float_type(d->c_type) ||
+        !float_type(d->scale_type) || (d->bias && !float_type(d->bias_type)) ||
+        d->act < DG_ACT_NONE || d->act > DG_ACT_GELU_TANH)
+        return DG_ERROR_INVALID_VALUE;
+    if (d->groups < 0 || d->M < 0 || d->N < 0 || d->K < 0 || d->lda < 1 || d->ldb < 1 || d->ldc < 1 ||
+        d->lda < d->K || d->ldb < d->K || d->ldc < d->N || d->stride_b < 0 || d->stride_s < 0 ||
+        (d->bias && d->stride_bias < 0))
+        return DG_ERROR_INVALID_VALUE;
+    if (d->groups > kMaxGroups || d->M > INT32_MAX || d->K > kMaxK)
+        return DG_ERROR_NOT_SUPPORTED;
+    s->offsets = (d->groups + 1) * 4;
+    s->bias = 0;
+    s->sa = d->M * 4;
+    const int64_t n_ld = d->N > 0 ? d->N : 1;
+    const bool ok =
+        bytes_of(1, 0, d->M, d->K, d->lda, a_bytes(d), &s->a) &&
+        bytes_of(d->groups, d->stride_b, d->N, d->K, d->ldb, 1, &s->b) &&
+        bytes_of(d->groups, d->stride_s, 1, d->N, n_ld, elem_size(d->scale_type), &s->sb) &&
+        bytes_of(1, 0, d->M, d->N, d->ldc, elem_size(d->c_type), &s->c) &&
+        (!d->bias || bytes_of(d->groups, d->stride_bias, 1, d->N, n_ld, elem_size(d->bias_type), &s->bias));
+    s->codes = d->a_type == DG_I8 ? 0 : d->M * codes_ld(d);          // below 2^31 * 2^18
+    s->workspace = d->a_type == DG_I8 ? 0 : s->codes + s->sa;
+    return ok ? DG_SUCCESS : DG_ERROR_INVALID_VALUE;
+}
+
+using ScaledLaunch = hipError_t (*)(const ScaledArgs &, uint32_t, hipStream_t);
+
+struct ScaledKernel {
+    const char *name;
+    int32_t bm, bn, threads;
+    bool any_alignment;
+    ScaledLaunch launch;
+};
+
+template <int V>
+hipError_t stream_kernel(const ScaledArgs &a, uint32_t p, hipStream_t s) { return launch_scaled_stream(V, a, p, s); }
+template <int V>
+hipError_t tile_kernel(const ScaledArgs &a, uint32_t p, hipStream_t s) { return launch_scaled_tile(V, a, p, s); }
+
+const ScaledKernel kS16x16 = {"i8_stream_16x16", 16, 16, 512, true, stream_kernel<0>};
+const ScaledKernel kS16x32 = {"i8_stream_16x32", 16, 32, 512, true, stream_kernel<1>};
+const ScaledKernel kS16x64 = {"i8_stream_16x64", 16, 64, 512, true, stream_kernel<2>};
+const ScaledKernel kS32x32 = {"i8_stream_32x32", 32, 32, 512, true, stream_kernel<3>};
+const ScaledKernel kS32x64 = {"i8_stream_32x64", 32, 64, 256, true, stream_kernel<4>};
+const ScaledKernel kS64x64 = {"i8_stream_64x64", 64, 64, 256, true, stream_kernel<5>};
+const ScaledKernel kT128 = {"i8_tile_128x128", 128, 128, 256, false, tile_kernel<0>};
+const ScaledKernel kT128x256 = {"i8_tile_128x256", 128, 256, 256, false, tile_kernel<1>};
+const ScaledKernel kT256 = {"i8_tile_256x256", 256, 256, 256, false, tile_kernel<2>};
+const ScaledKernel *const kKernels[] = {&kS16x16, &kS16x32, &kS16x64, &kS32x32, &kS32x64,
+                                        &kS64x64, &kT128, &kT128x256, &kT256};
+
+struct ScaledPlan {
+    const ScaledKernel *kernel;
+    uint32_t programs;
+};
+
+int64_t row_tiles(const dg_scaled_desc *d, int64_t bm)
+{
+    return d->groups > 1 ? d->M / bm + (d->groups < d->M ? d->groups : d->M) : ceil_div(d->M, bm);
+}
+
+// The tiles read whole 16-byte pieces and pairs of k, and address a tile
+// with 32-bit byte offsets.
+bool tile_ok(const dg_scaled_desc *d, const void *A, const void *B)
+{
+    const bool own = d->a_type != DG_I8;          // codes of the workspace
+    return (own || (aligned_to(A, 16) && d->lda % 16 == 0 && d->lda < (1 << 23))) && aligned_to(B, 16) &&
+           d->ldb % 16 == 0 && d->ldb < (1 << 23) && (d->groups <= 1 || d->stride_b % 16 == 0) && d->K % 2 == 0;
+}
+
+const ScaledKernel *choose(const dg_scaled_desc *d, bool tile)
+{
+    if (const char *want = getenv("DG_FORCE_GROUPED"))         // benchmarking and tests
+        for (const ScaledKernel *k : kKernels)
+            if (!strcmp(want, k->name) && (k->any_alignment || tile))
+                return k;
+    const int64_t rows = d->M / d->groups;
+    if (rows <= 16) {
+        const int64_t rt = row_tiles(d, 16);
+        return rt * ceil_div(d->N, 64) >= 512 ? &kS16x64 : rt * ceil_div(d->N, 32) >= 256 ? &kS16x32 : &kS16x16;
+    }
+    if (rows <= 32)
+        return row_tiles(d, 32) * ceil_div(d->N, 64) >= 256 ? &kS32x64 : &kS32x32;
+    if (!tile)
+        return &kS64x64;
+    if (row_tiles(d, 128) * ceil_div(d->N, 128) < 128)
+        return &kS32x64;
+    if (row_tiles(d, 256) * ceil_div(d->N, 256) >= 192)
+        return &kT256;
+    return row_tiles(d, 128) * ceil_div(d->N, 256) >= 192 ? &kT128x256 : &kT128;
+}
+
+dg_status make_plan(const dg_scaled_desc *d, const void *A, const void *B, ScaledPlan *p)
+{
+    const bool tile = tile_ok(d, A, B);
+    auto fits = [&](const ScaledKernel &k) {
+        int64_t n;
+        if ((!k.any_alignment && !tile) || !mul_ok(row_tiles(d, k.bm), ceil_div(d->N, k.bn), &n) ||
+            n > (int64_t)UINT32_MAX / k.threads)
+            return false;
+        p->programs = (uint32_t)n;
+        return true;
+    };
+    p->kernel = choose(d, tile);
+    if (fits(*p->kernel))
+        return DG_SUCCESS;
+    for (const ScaledKernel *k : kKernels)         // the next larger tile that a launch can have
+        if (k->bm * k->bn > p->kernel->bm * p->kernel->bn && fits(*k)) {
+            p->kernel = k;
+            return DG_SUCCESS;
+        }
+    return DG_ERROR_NOT_SUPPORTED;
+}
+
+} // namespace
+
+extern "C" {
+
+dg_status dg_gemm_scaled_workspace_size(const dg_scaled_desc *d, size_t *bytes)
+{
+    Spans sp;
+    const dg_status st = bytes ? validate(d, &sp) : DG_ERROR_INVALID_VALUE;
+    if (st == DG_SUCCESS)
+        *bytes = is_noop(d) || !reads_ab(d) ? 0 : (size_t)sp.workspace;
+    return st;
+}
+
+dg_status dg_gemm_scaled(const dg_scaled_desc *d, const void *A, const float *scale_a, const int8_t *B,
+                         const void *scale_b, void *C, const int32_t *offsets, void *workspace,
+                         size_t workspace_bytes, void *stream)
+{
+    Spans sp;
+    dg_status st = validate(d, &sp);
+    if (st != DG_SUCCESS)
+        return st;
+    const bool reads = reads_ab(d), make = d->a_type != DG_I8 && reads;
+    if ((!offsets && d->groups > 1) || (d->a_type != DG_I8 && scale_a))
+        return DG_ERROR_INVALID_VALUE;
+    if (is_noop(d))
+        return DG_SUCCESS;
+    if (!C || (reads && (!A || !B)))
+        return DG_ERROR_INVALID_VALUE;
+    if (!aligned_to(A, a_bytes(d)) || !aligned_to(scale_a, 4) || !aligned_to(scale_b, elem_size(d->scale_type)) ||
+        !aligned_to(C, elem_size(d->c_type)) || !aligned_to(offsets, 4) || !aligned_to(workspace, 16) ||
+        (d->bias && !aligned_to(d->bias, elem_size(d->bias_type))))
+        return DG_ERROR_INVALID_VALUE;
+    if (make && (!workspace || workspace_bytes < (size_t)sp.workspace))
+        return DG_ERROR_INSUFFICIENT_WORKSPACE;
+    const struct { const void *p; int64_t n; } others[] = {
+        {A, reads ? sp.a : 0}, {B, reads ? sp.b : 0}, {scale_a, reads ? sp.sa : 0}, {scale_b, reads ? sp.sb : 0},
+        {d->bias, sp.bias}, {offsets, sp.offsets}};
+    for (const auto &o : others)
+        if (ranges_overlap(C, sp.c, o.p, o.n) || (make && ranges_overlap(workspace, sp.workspace, o.p, o.n)))
+            return DG_ERROR_INVALID_VALUE;
+    if (make && ranges_overlap(workspace, sp.workspace, C, sp.c))
+        return DG_ERROR_INVALID_VALUE;
+    ScaledPlan p;
+    st = make_plan(d, A, B, &p);
+    if (st != DG_SUCCESS)
+        return st;
+
+    ScaledArgs a;
+    memset(&a, 0, sizeof a);
+    a.g.A = make ? workspace : A;
+    a.g.B = B;
+    a.g.C = C;
+    a.g.bias = d->bias;
+    a.g.N = d->N;
+    a.g.K = reads ? d->K : 0;
+    a.g.lda = make ? codes_ld(d) : d->lda;
+    a.g.ldb = d->ldb;
+    a.g.ldc = d->ldc;
+    a.g.sb = d->stride_b;
+    a.g.alpha = d->alpha;
+    a.g.beta = d->beta;
+    a.g.c_type = d->c_type;
+    a.g.bias_type = d->bias_type;
+    a.g.act = d->act;
+    a.g.ab_type = DT_I8;
+    if (d->alpha != 0.0f) {
+        a.scale_a = make ? (const float *)((char *)workspace + sp.codes) : scale_a;
+        a.scale_b = scale_b;
+    }
+    a.offsets = offsets;
+    a.groups = (int32_t)d->groups;
+    a.rows = (int32_t)d->M;
+    a.scale_type = d->scale_type;
+    a.stride_s = d->stride_s;
+    a.stride_bias = d->stride_bias;
+    a.tiles_n = (uint32_t)ceil_div(d->N, p.kernel->bn);
+    if (make) {
+        QuantizeArgs q;
+        memset(&q, 0, sizeof q);
+        q.x = (const char *)A;
+        q.q = (int8_t *)workspace;
+        q.scales = (float *)((char *)workspace + sp.codes);
+        q.ldx = d->lda * a_bytes(d);
+        q.ldq = codes_ld(d);
+        q.tokens = d->M;
+        q.width = d->K;
+        q.x_type = d->a_type;
+        if (launch_quantize(q, (hipStream_t)stream) != hipSuccess)
+            return DG_ERROR_LAUNCH;
+    }
+    return p.kernel->launch(a, p.programs, (hipStream_t)stream) == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
+}
+
+dg_status dg_gemm_scaled_describe(const dg_scaled_desc *d, char *buf, size_t len)
+{
+    if (!buf || len == 0)
+        return DG_ERROR_INVALID_VALUE;
+    Spans sp;
+    dg_status st = validate(d, &sp);
+    if (st != DG_SUCCESS)
+        return st;
+    if (is_noop(d)) {
+        snprintf(buf, len, "noop");
+        return DG_SUCCESS;
+    }
+    ScaledPlan p;
+    st = make_plan(d, nullptr, nullptr, &p);
+    if (st == DG_SUCCESS)
+        snprintf(buf, len, "kernel=%s bm=%d bn=%d programs=%u", p.kernel->name, p.kernel->bm, p.kernel->bn,
+                 p.programs);
+    return st;
+}
+
+} // extern "C"

@@ -65,7 +65,8 @@ typedef enum {
  * correctness check ("Skill: Write a Triton GEMM Kernel", Inputs the agent
  * should gather first, and the allclose check of "GEMM Kernel
  * Optimization", Verification). */
-typedef enum { DG_F32 = 0, DG_BF16 = 1, DG_F16 = 2 } dg_dtype;
+/* DG_I8, signed 8-bit integers, is a type of dg_gemm_scaled's A only. */
+typedef enum { DG_F32 = 0, DG_BF16 = 1, DG_F16 = 2, DG_I8 = 3 } dg_dtype;
 
 /* Storage order of one operand.  Row-major X (R x C) with leading dimension
  * ld holds X[r][c] at element r*ld + c; column-major holds it at c*ld + r. */
@@ -513,6 +514,59 @@ typedef struct dg_quantize_desc {
 
 dg_status dg_quantize(const dg_quantize_desc *d, const void *x, const int32_t *place, int8_t *q,
                       float *scales, void *stream);
+
+/* The product of 8-bit integers with a scale for each row and each column:
+ *
+ *     C = act( alpha * scale_a[m] * scale_b[n] * sum_k A[m][k] * B[n][k]
+ *              + beta * C + bias )
+ *
+ * with A M x K and B N x K (one row per column of C), both row-major, C M x N
+ * row-major.  The sum is exact, in 32-bit integers; it is converted to fp32
+ * (half a step of 24 bits) and multiplied by scale_a, scale_b and alpha in
+ * that order.  scale_a (fp32) or scale_b NULL: ones.
+ * a_type F32, BF16 or F16: A's rows are turned into codes and scales first,
+ * as by dg_quantize, in the workspace; scale_a must be NULL.
+ * With offsets, row i of A and C uses the B of the group that holds it, B + e
+ * * stride_b, scale_b + e * stride_s, bias + e * stride_bias; the offsets as
+ * in dg_gemm_grouped with M in the place of rows, and rows of no group left
+ * as they were.  offsets may be NULL when groups == 1: all M rows then use
+ * the one B.
+ *
+ *   struct_size  sizeof(dg_scaled_desc).
+ *   a_type       DG_I8 or any other dg_dtype (see above).
+ *   c_type, scale_type (of scale_b), bias_type   F32, BF16 or F16.
+ *   groups       1 .. 65536 matrices B (0 is a no-op).
+ *   M            0 .. 2^31 - 1 rows.
+ *   K            0 .. 131071 (more: DG_ERROR_NOT_SUPPORTED; the sum would not
+ *                fit 32 bits).
+ *   lda, ldb >= max(1, K), ldc >= max(1, N); strides >= 0, in elements. */
+typedef struct dg_scaled_desc {
+    uint32_t struct_size;
+    int32_t a_type, c_type, scale_type, bias_type;
+    int32_t act;
+    int64_t groups;
+    int64_t M, N, K;
+    int64_t lda, ldb, ldc;
+    int64_t stride_b, stride_s, stride_bias;
+    float alpha, beta;
+    const void *bias;
+} dg_scaled_desc;
+
+/* Device bytes of workspace of dg_gemm_scaled: 0 for a_type DG_I8. */
+dg_status dg_gemm_scaled_workspace_size(const dg_scaled_desc *d, size_t *bytes);
+
+/* Enqueue the product on `stream`; may be captured.  workspace: 16-byte
+ * aligned, used until the call's work has completed; fewer bytes than
+ * dg_gemm_scaled_workspace_size says are DG_ERROR_INSUFFICIENT_WORKSPACE.
+ * DG_ERROR_NOT_SUPPORTED also where even the largest tile makes a launch of
+ * 2^32 threads or more. */
+dg_status dg_gemm_scaled(const dg_scaled_desc *d, const void *A, const float *scale_a,
+                         const int8_t *B, const void *scale_b, void *C, const int32_t *offsets,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/* One line on the kernel, tile and grid dg_gemm_scaled would run, with or
+ * without offsets (operands taken as aligned). */
+dg_status dg_gemm_scaled_describe(const dg_scaled_desc *d, char *buf, size_t len);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,128 @@
+"""dg_gemm_scaled on the host: the struct mirrors the header, every invalid
+descriptor or pointer is refused before anything is enqueued, shapes without
+work succeed, plans follow the stated rules."""
+import ctypes
+import os
+import subprocess
+import tempfile
+
+import pytest
+import torch
+
+import dense_gemm_10_amd as dg
+from conftest import ROOT
+from dense_gemm_10_amd import scaled as S
+
+HEADER = os.path.join(ROOT, "include", "densegemm.h")
+PA, PSA, PB, PSB, PC, PO, PW, PX = (i << 56 for i in range(1, 9))      # never dereferenced
+BAD, NO, OK, SHORT = (dg.DG_ERROR_INVALID_VALUE, dg.DG_ERROR_NOT_SUPPORTED, dg.DG_SUCCESS,
+                      dg.DG_ERROR_INSUFFICIENT_WORKSPACE)
+
+
+def test_struct_layout_matches_header():
+    fields = [f for f, _ in dg.DgScaledDesc._fields_]
+    src = ["#include <stdio.h>", "#include <stddef.h>", f'#include "{HEADER}"', "int main(void) {",
+           'printf("%zu\\n", sizeof(dg_scaled_desc));']
+    src += [f'printf("%zu\\n", offsetof(dg_scaled_desc, {f}));' for f in fields]
+    src += ['printf("%d\\n", DG_I8);', "return 0; }"]
+    with tempfile.TemporaryDirectory() as d:
+        c, exe = os.path.join(d, "layout.c"), os.path.join(d, "layout")
+        open(c, "w").write("\n".join(src))
+        subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", c, "-o", exe], check=True)
+        vals = [int(v) for v in subprocess.run([exe], capture_output=True, text=True,
+                                               check=True).stdout.split()]
+    assert vals[0] == ctypes.sizeof(dg.DgScaledDesc) and vals[-1] == dg.DG_I8
+    assert [getattr(dg.DgScaledDesc, f).offset for f in fields] == vals[1:-1]
+
+
+def test_packed_descriptor_matches_the_structure():
+    n = len(dg.DgScaledDesc._fields_) - 4
+    values = [S._SIZE, *range(1, n + 1), 1.5, -0.25, 0x1234567890]
+    assert S._pack(*values) == bytes(dg.DgScaledDesc(*values))
+
+
+def _d(**kw):
+    return dg.make_scaled_desc(**dict(dict(M=5, N=48, K=64), **kw))
+
+
+def _run(d, A=PA, sa=PSA, B=PB, sb=PSB, C=PC, off=None, ws=None, n=0):
+    return dg.dg_gemm_scaled(d, A, sa, B, sb, C, off, ws, n, check=False)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(M=-1), BAD), (dict(N=-1, ldc=1), BAD), (dict(K=-1), BAD), (dict(groups=-1), BAD), (dict(a_type=4), BAD),
+    (dict(a_type=-1), BAD), (dict(c_type=3), BAD), (dict(scale_type=3), BAD), (dict(act=3), BAD),
+    (dict(lda=63), BAD), (dict(ldb=63), BAD), (dict(ldc=47), BAD), (dict(stride_b=-1), BAD), (dict(stride_s=-1), BAD),
+    (dict(bias=PX, bias_type=3), BAD), (dict(bias=PX, stride_bias=-1), BAD), (dict(groups=2), BAD),
+    (dict(N=2 ** 45, ldb=2 ** 40, ldc=2 ** 45), BAD), (dict(groups=65537), NO), (dict(M=2 ** 31), NO),
+    (dict(K=131072), NO), (dict(lda=2 ** 62, M=2 ** 31 - 1), BAD),
+], ids=str)
+def test_invalid_descriptors(kw, want):
+    d = _d(**kw)
+    assert _run(d, off=PO if kw.get("groups", 1) > 2 else None) == want       # groups = 2 lacks offsets
+    if kw != dict(groups=2):
+        for f in (dg.dg_gemm_scaled_describe, dg.dg_gemm_scaled_workspace_size):
+            with pytest.raises(dg.DgError) as e:
+                f(d)
+            assert e.value.status == want
+
+
+def test_pointers():
+    d = _d()
+    for kw in (dict(A=None), dict(B=None), dict(C=None), dict(sa=PSA + 2), dict(sb=PSB + 1), dict(C=PC + 1),
+               dict(off=PO + 2), dict(ws=PW + 8, n=100), dict(C=PA), dict(C=PB + 32), dict(C=PSA), dict(C=PSB - 8),
+               dict(off=PC)):
+        assert _run(d, **kw) == BAD, kw
+    assert _run(_d(bias=PC + 4)) == BAD and _run(_d(bias=PX + 2)) == BAD
+    d.struct_size = 8
+    assert _run(d) == BAD
+
+
+def test_workspace_of_a_float_operand():
+    d = _d(a_type="bf16", K=70)
+    need = dg.dg_gemm_scaled_workspace_size(d)
+    assert need == 5 * 80 + 5 * 4
+    assert dg.dg_gemm_scaled_workspace_size(_d()) == 0
+    assert dg.dg_gemm_scaled_workspace_size(_d(a_type="bf16", alpha=0.0)) == 0
+    assert _run(d, sa=PSA) == BAD
+    assert _run(d, sa=None) == SHORT and _run(d, sa=None, ws=PW, n=need - 1) == SHORT
+    assert _run(d, sa=None, A=PA + 1, ws=PW, n=need) == BAD
+    for other in (dict(C=PW + 16), dict(B=PW), dict(A=PW), dict(sb=PW)):
+        assert _run(d, **{"sa": None, "ws": PW, "n": need, **other}) == BAD, other
+
+
+def test_shapes_without_work():
+    for kw in (dict(M=0), dict(N=0), dict(groups=0)):
+        assert _run(_d(**kw), None, None, None, None, None) == OK
+        assert dg.dg_gemm_scaled_describe(_d(**kw)) == "noop"
+
+
+def _t(*shape, dtype=torch.int8):
+    return torch.zeros(shape, dtype=dtype)
+
+
+OFF = torch.zeros(4, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("what,call,match", [
+    ("inner sizes", lambda: dg.gemm_scaled(_t(4, 8), _t(6, 9)), "wanted"),
+    ("B with groups alone", lambda: dg.gemm_scaled(_t(4, 8), _t(3, 6, 8)), "wanted"),
+    ("offsets alone", lambda: dg.gemm_scaled(_t(4, 8), _t(6, 8), offsets=OFF), "wanted"),
+    ("B's type", lambda: dg.gemm_scaled(_t(4, 8), _t(6, 8, dtype=torch.uint8)), "int8"),
+    ("scale_a of a float A", lambda: dg.gemm_scaled(_t(4, 8, dtype=torch.float32), _t(6, 8),
+                                                    _t(4, dtype=torch.float32)), "scale_a"),
+    ("scale_a's type", lambda: dg.gemm_scaled(_t(4, 8), _t(6, 8), _t(4, dtype=torch.bfloat16)), "scale_a"),
+    ("scale_a's size", lambda: dg.gemm_scaled(_t(4, 8), _t(6, 8), _t(5, dtype=torch.float32)), "scale_a"),
+    ("scale_b's size", lambda: dg.gemm_scaled(_t(4, 8), _t(6, 8), None, _t(5, dtype=torch.float32)), "scale_b"),
+    ("scale_b strided", lambda: dg.gemm_scaled(_t(4, 8), _t(6, 8), None, _t(12, dtype=torch.float32)[::2]),
+     "scale_b"),
+    ("groups of offsets", lambda: dg.gemm_scaled(_t(4, 8), _t(2, 6, 8), offsets=OFF), "offsets"),
+    ("beta without C", lambda: dg.gemm_scaled(_t(4, 8), _t(6, 8), beta=1.0), "beta"),
+    ("C's shape", lambda: dg.gemm_scaled(_t(4, 8), _t(6, 8), None, None, _t(4, 5, dtype=torch.float32)), "C"),
+    ("bias' shape", lambda: dg.gemm_scaled(_t(4, 8), _t(6, 8), None, None, _t(4, 6, dtype=torch.float32),
+                                           bias=_t(5, dtype=torch.float32)), None),
+    ("on the CPU", lambda: dg.gemm_scaled(_t(4, 8), _t(6, 8)), "GPU"),
+], ids=lambda v: v if isinstance(v, str) else "")
+def test_torch_entry_point_refuses(what, call, match):
+    with pytest.raises(ValueError, match=match):
+        call()
