@@ -183,6 +183,28 @@ __device__ __forceinline__ const f32x4_t &acc_block16(const Acc16View<FM, FN> &v
     return v.a[i][j];
 }
 
+// A wave's 16 x 16 blocks of exact sums, as the epilogue takes them: to fp32
+// and times the scales block by block as they are staged.
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+template <int FM, int FN>
+struct ScaledView {
+    const i32x4_t (&a)[FM][FN];
+    const float *rows;         // in LDS: of the lane's first row of block 0
+    float cols[FN];            // of the lane's column of each block
+};
+template <int FM, int FN> struct acc_traits<ScaledView<FM, FN>> { static constexpr int MS = 16; };
+
+template <int FM, int FN>
+__device__ __forceinline__ f32x4_t acc_block16(const ScaledView<FM, FN> &v, int i, int j)
+{
+    const f32x4_t r = *(const f32x4_t *)(v.rows + 16 * i);
+    f32x4_t out;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        out[e] = (float)v.a[i][j][e] * r[e] * v.cols[j];
+    return out;
+}
+
 // The epilogue reads a wave's accumulators one block at a time: FM x FN
 // 32 x 32 blocks in the 32 x 32 MFMA register layout through acc_block, or,
 // for an Acc16View (acc_traits MS = 16), 2FM x 2FN 16 x 16 blocks through

@@ -13,29 +13,17 @@ namespace dg {
 
 namespace {
 
-struct Piece { uint32_t w[4]; };
-
 __device__ __forceinline__ i32x4_t load_piece(const int8_t *p)
 {
-    Piece r;
-    __builtin_memcpy(&r, p, 16);
-    return __builtin_bit_cast(i32x4_t, r);
+    return __builtin_bit_cast(i32x4_t, load_bytes16(p));
 }
 
-// Bytes k .. k + 15 of a row of K, zero from K on.
 __device__ __forceinline__ i32x4_t load_piece_masked(const int8_t *row, int64_t k, int64_t K)
 {
-    if (k + 16 <= K)
-        return load_piece(row + k);
-    Piece r{};
-#pragma unroll
-    for (int i = 0; i < 15; ++i)
-        if (k + i < K)
-            r.w[i / 4] |= (uint32_t)(uint8_t)row[k + i] << (8 * (i % 4));
-    return __builtin_bit_cast(i32x4_t, r);
+    return __builtin_bit_cast(i32x4_t, load_masked16(row, k, K));
 }
 
-template <int FM, int FN, int KW>
+template <int FM, int FN, int KW, int D>
 __global__ __launch_bounds__(64 * KW) void scaled_stream_kernel(ScaledArgs a)
 {
     constexpr int SK = 128, NT = 64 * KW, TILE = 16 * FM * 16 * FN, LD = 16 * FN + 4;
@@ -89,25 +77,36 @@ __global__ __launch_bounds__(64 * KW) void scaled_stream_kernel(ScaledArgs a)
     };
 
     if (g.alpha != 0.0f) {
-        const int64_t full = g.K / SK;
-        int64_t s = wave;
+        // A ring of D steps in registers, so that D steps' loads are under way
+        // while one is multiplied.  Loads past the last whole step repeat it
+        // and are not used: with none left out, the compiler can count them.
+        const int32_t full = (int32_t)(g.K / SK);
+        int32_t s = wave;
         if (s < full) {
-            Step now, next;
-            load(now, s * SK);
-            for (; s + KW < full; s += KW) {
-                load(next, (s + KW) * SK);
-                multiply(now);
-                now = next;
+            Step ring[D];
+            auto fetch = [&](Step &r, int32_t at) { load(r, (int64_t)(at < full ? at : full - 1) * SK); };
+#pragma unroll
+            for (int i = 0; i < D; ++i)
+                fetch(ring[i], s + i * KW);
+            for (; s + D * KW < full; s += D * KW) {
+#pragma unroll
+                for (int i = 0; i < D; ++i) {
+                    multiply(ring[i]);
+                    fetch(ring[i], s + (D + i) * KW);
+                }
             }
-            multiply(now);
-            s += KW;
+#pragma unroll
+            for (int i = 0; i < D; ++i)
+                if (s + i * KW < full)
+                    multiply(ring[i]);
         }
-        // at most one step is left, and one wavefront's turn
-        if (s * SK < g.K) {
+        // at most one step is left, the turn of wavefront full mod KW
+        const int64_t k0 = (int64_t)full * SK;
+        if (k0 < g.K && wave == full % KW) {
             Step last;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int64_t k = s * SK + 64 * h + 16 * kg;
+                const int64_t k = k0 + 64 * h + 16 * kg;
 #pragma unroll
                 for (int j = 0; j < FN; ++j)
                     last.b[h][j] = load_piece_masked(bp[j], k, g.K);
@@ -144,11 +143,11 @@ __global__ __launch_bounds__(64 * KW) void scaled_stream_kernel(ScaledArgs a)
     }
 }
 
-template <int FM, int FN, int KW>
+template <int FM, int FN, int KW, int D>
 hipError_t launch(const ScaledArgs &a, uint32_t programs, hipStream_t s)
 {
     constexpr size_t lds = (size_t)KW * 16 * FM * (16 * FN + 4) * 4;
-    hipLaunchKernelGGL((scaled_stream_kernel<FM, FN, KW>), dim3(programs), dim3(64 * KW), lds, s, a);
+    hipLaunchKernelGGL((scaled_stream_kernel<FM, FN, KW, D>), dim3(programs), dim3(64 * KW), lds, s, a);
     return hipGetLastError();
 }
 
@@ -157,12 +156,11 @@ hipError_t launch(const ScaledArgs &a, uint32_t programs, hipStream_t s)
 hipError_t launch_scaled_stream(int32_t variant, const ScaledArgs &a, uint32_t programs, hipStream_t s)
 {
     switch (variant) {
-    case 0: return launch<1, 1, 8>(a, programs, s);
-    case 1: return launch<1, 2, 8>(a, programs, s);
-    case 2: return launch<1, 4, 8>(a, programs, s);
-    case 3: return launch<2, 2, 8>(a, programs, s);
-    case 4: return launch<2, 4, 4>(a, programs, s);
-    case 5: return launch<4, 4, 4>(a, programs, s);
+    case 0: return launch<1, 1, 8, 2>(a, programs, s);
+    case 1: return launch<1, 2, 8, 2>(a, programs, s);
+    case 2: return launch<1, 4, 8, 2>(a, programs, s);
+    case 3: return launch<2, 2, 8, 2>(a, programs, s);
+    case 4: return launch<2, 4, 8, 2>(a, programs, s);
     default: return hipErrorInvalidValue;
     }
 }

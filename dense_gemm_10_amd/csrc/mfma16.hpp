@@ -82,7 +82,6 @@ typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 // Fragment type of element type T, and the 32 x 32 x 16 MFMA on it.
 template <int T> struct frag_of { using type = bf16x8_t; };
 template <> struct frag_of<DT_F16> { using type = f16x8_t; };
-typedef int i32x4_t __attribute__((ext_vector_type(4)));
 template <> struct frag_of<DT_I8> { using type = i32x4_t; };     // 16 of them
 
 __device__ __forceinline__ f32x16_t mfma_32x32x16(bf16x8_t a, bf16x8_t b, f32x16_t c)
@@ -323,6 +322,31 @@ __device__ __forceinline__ frag_t tr_fragment(uint32_t addr0)
         __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4)(uintptr_t)(addr0 + 4 * ROW_BYTES));
     const s16x8_t both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     return __builtin_bit_cast(frag_t, both);
+}
+
+// Epilogue of a tile of exact sums (16 x 16 blocks): the rows' scales go to
+// LDS behind the epilogue's own part, the columns' into registers.
+constexpr int scaled_epilogue_lds_bytes(int BM, int BN) { return epilogue_lds_bytes(BN, 16) + BM * 4; }
+
+template <int BM, int BN, int WM, int WN, int REGS, int FM, int FN>
+__device__ __forceinline__ void scaled_epilogue(const GemmArgs &g, const TileCoord &tc, float *lds, int64_t m0,
+                                                int64_t n0, const i32x4_t (&acc)[FM][FN],
+                                                const RowColScales &scales)
+{
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t last_row = (g.M - m0 < BM ? g.M - m0 : BM) - 1, last_col = (g.N - n0 < BN ? g.N - n0 : BN) - 1;
+    float *row_s = lds + epilogue_lds_bytes(BN, 16) / 4;
+    for (int r = tid; r < BM; r += 64 * WM * WN)
+        row_s[r] = scales.rows ? scales.rows[m0 + (r < last_row ? r : last_row)] : 1.0f;
+    ScaledView<FM, FN> view{acc, row_s + wave / WN * (BM / WM) + 4 * (lane >> 4), {}};
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+        const int64_t c = wave % WN * (BN / WN) + 16 * j + (lane & 15);
+        view.cols[j] = scales.cols ? load_as_f32(scales.cols, scales.cols_type, n0 + (c < last_col ? c : last_col))
+                                   : 1.0f;
+    }
+    lds_barrier();
+    tile_epilogue<BM, BN, WM, WN, REGS>(g, tc, lds, m0, n0, view);
 }
 
 // One output tile (or, for stream-K, one K range of it): K loop over
@@ -684,8 +708,9 @@ __device__ __forceinline__ void mfma16_tile(const GemmArgs &g, TileCoord tc, int
         barrier();
     }
 
-    // the epilogue keeps within the kernel's register budget
-    constexpr int REGS = 512 / mfma16_per_cu(BM, BN, kStages, MBK);
+    // the epilogue keeps within the kernel's register budget; the kernels of
+    // 8-bit products have half the register file, whatever LDS allows
+    constexpr int REGS = T == DT_I8 ? 256 : 512 / mfma16_per_cu(BM, BN, kStages, MBK);
     if constexpr (MS == 32) {
         if (part)
             tile_epilogue_rows<BM, BN, WM, WN, true, DT_F32, REGS, false>(
@@ -693,28 +718,9 @@ __device__ __forceinline__ void mfma16_tile(const GemmArgs &g, TileCoord tc, int
         else
             tile_epilogue<BM, BN, WM, WN, REGS>(g, tc, (float *)lds, m0, n0, acc);
     } else if constexpr (T == DT_I8) {
-        // the exact sums to fp32, times the scales of their row and column
-        f32x4_t f[FM][FN];
-        float sc[FN];
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            const int64_t c = wn * TN + MS * j + frag_row;
-            sc[j] = scales.cols ? load_as_f32(scales.cols, scales.cols_type, n0 + (c < b_ext ? c : b_ext - 1))
-                                : 1.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < FM; ++i) {
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int64_t r = wm * TM + MS * i + 4 * frag_grp + v;
-                const float sr = scales.rows ? scales.rows[m0 + (r < a_ext ? r : a_ext - 1)] : 1.0f;
-#pragma unroll
-                for (int j = 0; j < FN; ++j)
-                    f[i][j][v] = (float)acc[i][j][v] * sr * sc[j];
-            }
-        }
-        const Acc16View<FM, FN> view{f};
-        tile_epilogue<BM, BN, WM, WN, REGS>(g, tc, (float *)lds, m0, n0, view);
+        static_assert(scaled_epilogue_lds_bytes(BM, BN) <= mfma16_lds_bytes(BM, BN, kStages, MBK, MS),
+                      "room for the scales");
+        scaled_epilogue<BM, BN, WM, WN, REGS>(g, tc, (float *)lds, m0, n0, acc, scales);
     } else {
         const Acc16View<FM, FN> view{acc};
         if (part)

@@ -67,6 +67,40 @@ __device__ __forceinline__ const void *col_scales(const ScaledArgs &a, int32_t e
     return a.scale_b ? (const char *)a.scale_b + e * a.stride_s * (a.scale_type == DT_F32 ? 4 : 2) : nullptr;
 }
 
+// 16 bytes of a row from any address (gfx950 loads them so).
+struct Bytes16 { uint32_t w[4]; };
+
+__device__ __forceinline__ Bytes16 load_bytes16(const int8_t *p)
+{
+    Bytes16 r;
+    __builtin_memcpy(&r, p, 16);
+    return r;
+}
+
+// Bytes k .. k + 15 of a row of K, zero from K on, and nothing read past K.
+// Where K cuts them, the row's last 16 bytes are loaded and moved down.
+__device__ __forceinline__ Bytes16 load_masked16(const int8_t *row, int64_t k, int64_t K)
+{
+    if (k + 16 <= K)
+        return load_bytes16(row + k);
+    if (k >= K)
+        return Bytes16{};
+    if (K < 16) {
+        Bytes16 r{};
+#pragma unroll
+        for (int i = 0; i < 15; ++i)               // k is 0 then
+            if (i < K)
+                r.w[i / 4] |= (uint32_t)(uint8_t)row[i] << (8 * (i % 4));
+        return r;
+    }
+    const Bytes16 end = load_bytes16(row + K - 16);
+    const int by = 8 * (16 - (int)(K - k));        // bits to go: 8 .. 120
+    uint64_t lo = end.w[0] | (uint64_t)end.w[1] << 32, hi = end.w[2] | (uint64_t)end.w[3] << 32;
+    lo = by >= 64 ? hi >> (by - 64) : lo >> by | hi << (64 - by);
+    hi = by >= 64 ? 0 : hi >> by;
+    return Bytes16{{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)}};
+}
+
 // Launchers; each returns hipSuccess or the launch error.
 hipError_t launch_scaled_stream(int32_t variant, const ScaledArgs &a, uint32_t programs, hipStream_t s);
 hipError_t launch_scaled_tile(int32_t variant, const ScaledArgs &a, uint32_t programs, hipStream_t s);

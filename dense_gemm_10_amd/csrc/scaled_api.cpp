@@ -90,13 +90,14 @@ const ScaledKernel kS16x16 = {"i8_stream_16x16", 16, 16, 512, true, stream_kerne
 const ScaledKernel kS16x32 = {"i8_stream_16x32", 16, 32, 512, true, stream_kernel<1>};
 const ScaledKernel kS16x64 = {"i8_stream_16x64", 16, 64, 512, true, stream_kernel<2>};
 const ScaledKernel kS32x32 = {"i8_stream_32x32", 32, 32, 512, true, stream_kernel<3>};
-const ScaledKernel kS32x64 = {"i8_stream_32x64", 32, 64, 256, true, stream_kernel<4>};
-const ScaledKernel kS64x64 = {"i8_stream_64x64", 64, 64, 256, true, stream_kernel<5>};
-const ScaledKernel kT128 = {"i8_tile_128x128", 128, 128, 256, false, tile_kernel<0>};
-const ScaledKernel kT128x256 = {"i8_tile_128x256", 128, 256, 256, false, tile_kernel<1>};
-const ScaledKernel kT256 = {"i8_tile_256x256", 256, 256, 256, false, tile_kernel<2>};
+const ScaledKernel kS32x64 = {"i8_stream_32x64", 32, 64, 512, true, stream_kernel<4>};
+const ScaledKernel kAny64 = {"i8_any_64x128", 64, 128, 256, true, tile_kernel<0>};
+const ScaledKernel kAny128 = {"i8_any_128x128", 128, 128, 256, true, tile_kernel<1>};
+const ScaledKernel kT128deep = {"i8_tile_128x128_deep", 128, 128, 512, false, tile_kernel<2>};
+const ScaledKernel kT128 = {"i8_tile_128x128", 128, 128, 512, false, tile_kernel<3>};
+const ScaledKernel kT256 = {"i8_tile_256x256", 256, 256, 512, false, tile_kernel<4>};
 const ScaledKernel *const kKernels[] = {&kS16x16, &kS16x32, &kS16x64, &kS32x32, &kS32x64,
-                                        &kS64x64, &kT128, &kT128x256, &kT256};
+                                        &kAny64, &kAny128, &kT128deep, &kT128, &kT256};
 
 struct ScaledPlan {
     const ScaledKernel *kernel;
@@ -117,26 +118,65 @@ bool tile_ok(const dg_scaled_desc *d, const void *A, const void *B)
            d->ldb % 16 == 0 && d->ldb < (1 << 23) && (d->groups <= 1 || d->stride_b % 16 == 0) && d->K % 2 == 0;
 }
 
+// Tiles of bm x bn that a launch has to do, about: group lengths are unknown,
+// and half the groups are taken to end in one more tile.
+double expected_tiles(const dg_scaled_desc *d, int64_t bm, int64_t bn)
+{
+    const double rt = d->groups > 1 ? (double)d->M / (double)bm + 0.5 * (double)d->groups
+                                    : (double)ceil_div(d->M, bm);
+    return rt * (double)ceil_div(d->N, bn);
+}
+
+// The kernel for a problem, by the mean rows of a group (us, MI355X, int8 in,
+// bf16 out, B from memory; M x N x K):
+//   up to 16 (8 with groups), the 16-row streaming kernels, the widest that
+//     still makes enough workgroups: 1 x 4096 x 4096 6.1 on 16 columns, 7.7 on
+//     32, 11.2 on 64; 1 x 6000 x 4096 8.4, 7.7, 11.3; 16 x 8192 x 8192 20.4,
+//     17.6, 24.7; 13 x 16384 x 8192 36.3, 37.8, 30.1; 64 rows, 64 groups, 2048
+//     x 2048 32.2, 31.1, 30.3; 8 rows, 8 groups, 1024 x 1024 6.2, 6.0, 7.7;
+//   then 32-row ones while they are one workgroup per compute unit: 64 x 4096 x
+//     4096 11.5 on 32 x 32, 15.5 on 32 x 64, 17.7 on 128 x 128; 64 x 8192 x
+//     4096 18.8, 16.1, 19.0; 128 x 8192 x 4096 33.0, 28.9, 20.2; groups of 9
+//     to 16 rows 32 x 32 unless 128 x 128 tiles fill the chip twice (100 rows,
+//     8 groups, 4096 x 4096 33.3 against 35.8; 1024 rows, 64 groups, 2048 x
+//     2048 80 against 57.6, and 74 on 16 x 64);
+//   128 x 128 with a ring of four stages, one workgroup per compute unit, up
+//     to 256 tiles (1024 x 4096 x 4096 21.3 against 27.2 with two stages and
+//     30.3 on 256 x 256), with two stages and two workgroups above (2000 rows,
+//     16 groups, 4096 x 2048 46.9 against 48.9 and 51.4);
+//   256 x 256, cut in halves where that saves a wave, from half a chip of
+//     them, with groups of 256 rows from a whole chip (2048 x 4096 x 4096 35.1
+//     against 36.4 on 128 x 128; 4096 x 4096 x 4096 56 against 70; 8192 rows,
+//     16 groups, 4096 x 4096 168 against 195; but 8192 rows, 8 groups, 1024 x
+//     4096, 144 of them, 61 against 59).
+// Off the 16-byte grid, or with odd K: the same streaming kernels, then tiles
+// filled through registers, 64 x 128 until 128 x 128 ones fill the chip twice
+// (700 x 4097 x 1001 19 against 20, and 89 on 32 x 64; 2048 x 4096 x 4096 92
+// against 67).
 const ScaledKernel *choose(const dg_scaled_desc *d, bool tile)
 {
     if (const char *want = getenv("DG_FORCE_GROUPED"))         // benchmarking and tests
         for (const ScaledKernel *k : kKernels)
             if (!strcmp(want, k->name) && (k->any_alignment || tile))
                 return k;
-    const int64_t rows = d->M / d->groups;
-    if (rows <= 16) {
+    const bool groups = d->groups > 1;
+    const double mean = (double)d->M / (double)d->groups;
+    if (mean <= (groups ? 8 : 16)) {
         const int64_t rt = row_tiles(d, 16);
-        return rt * ceil_div(d->N, 64) >= 512 ? &kS16x64 : rt * ceil_div(d->N, 32) >= 256 ? &kS16x32 : &kS16x16;
+        return rt * ceil_div(d->N, 64) >= (groups ? 512 : 256) ? &kS16x64
+               : rt * ceil_div(d->N, 32) >= 160                ? &kS16x32
+                                                               : &kS16x16;
     }
-    if (rows <= 32)
-        return row_tiles(d, 32) * ceil_div(d->N, 64) >= 256 ? &kS32x64 : &kS32x32;
+    const double t128 = expected_tiles(d, 128, 128), t256 = expected_tiles(d, 256, 256);
+    if (groups ? mean <= 16 && t128 <= 512 : expected_tiles(d, 32, 32) <= 256)
+        return &kS32x32;
     if (!tile)
-        return &kS64x64;
-    if (row_tiles(d, 128) * ceil_div(d->N, 128) < 128)
+        return t128 >= 512 ? &kAny128 : &kAny64;
+    if (!groups && expected_tiles(d, 32, 64) <= 256)
         return &kS32x64;
-    if (row_tiles(d, 256) * ceil_div(d->N, 256) >= 192)
+    if (groups ? mean >= 256 && t256 >= 256 : t256 >= 128)
         return &kT256;
-    return row_tiles(d, 128) * ceil_div(d->N, 256) >= 192 ? &kT128x256 : &kT128;
+    return t128 <= 256 ? &kT128deep : &kT128;
 }
 
 dg_status make_plan(const dg_scaled_desc *d, const void *A, const void *B, ScaledPlan *p)
@@ -145,7 +185,7 @@ dg_status make_plan(const dg_scaled_desc *d, const void *A, const void *B, Scale
     auto fits = [&](const ScaledKernel &k) {
         int64_t n;
         if ((!k.any_alignment && !tile) || !mul_ok(row_tiles(d, k.bm), ceil_div(d->N, k.bn), &n) ||
-            n > (int64_t)UINT32_MAX / k.threads)
+            n > (int64_t)UINT32_MAX / k.threads - 128)      // launch_mixed adds 128
             return false;
         p->programs = (uint32_t)n;
         return true;

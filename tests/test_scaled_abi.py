@@ -126,3 +126,49 @@ OFF = torch.zeros(4, dtype=torch.int32)
 def test_torch_entry_point_refuses(what, call, match):
     with pytest.raises(ValueError, match=match):
         call()
+
+
+# ---- the kernel a problem gets ------------------------------------------------------
+def _plan(text):
+    p = dict(t.split("=") for t in text.split())
+    return p["kernel"], int(p["programs"])
+
+
+@pytest.mark.parametrize("M,N,K,kw,kernel", [
+    (1, 4096, 4096, {}, "i8_stream_16x16"), (16, 8192, 8192, {}, "i8_stream_16x32"),
+    (13, 16384, 8192, {}, "i8_stream_16x64"), (64, 4096, 4096, {}, "i8_stream_32x32"),
+    (64, 8192, 4096, {}, "i8_stream_32x64"), (128, 8192, 4096, {}, "i8_tile_128x128_deep"),
+    (1024, 4096, 4096, {}, "i8_tile_128x128_deep"), (2048, 2560, 1024, {}, "i8_tile_128x128"),
+    (2048, 4096, 4096, {}, "i8_tile_256x256"),
+    (8, 1024, 1024, dict(groups=8), "i8_stream_16x32"), (64, 2048, 2048, dict(groups=64), "i8_stream_16x64"),
+    (100, 4096, 4096, dict(groups=8), "i8_stream_32x32"), (1024, 2048, 2048, dict(groups=64), "i8_tile_128x128"),
+    (400, 4096, 1024, dict(groups=8), "i8_tile_128x128_deep"), (8192, 4096, 4096, dict(groups=16), "i8_tile_256x256"),
+    (700, 4097, 1001, {}, "i8_any_64x128"), (2048, 4096, 4095, {}, "i8_any_128x128"),
+    (2048, 4096, 4095, dict(lda=4096, ldb=4096), "i8_any_128x128"),          # odd K
+    (2048, 4096, 4094, dict(lda=4096, ldb=4096), "i8_tile_256x256"),
+    (2048, 4096, 4096, dict(ldb=4104), "i8_any_128x128"), (2048, 4096, 4096, dict(lda=4104), "i8_any_128x128"),
+    (2048, 4096, 4096, dict(lda=4104, a_type="bf16"), "i8_tile_256x256"),      # the workspace's codes
+    (8192, 4096, 4096, dict(groups=16, stride_b=4096 * 4096 + 8), "i8_any_128x128"),
+    (64, 4097, 1001, {}, "i8_any_64x128"), (17, 4097, 1001, {}, "i8_stream_32x32"),
+], ids=str)
+def test_kernel_of_a_problem(M, N, K, kw, kernel, monkeypatch):
+    monkeypatch.delenv("DG_FORCE_GROUPED", raising=False)
+    assert _plan(dg.dg_gemm_scaled_describe(dg.make_scaled_desc(M, N, K, **kw)))[0] == kernel
+
+
+@pytest.mark.parametrize("M,N,kw,kernel", [
+    (16, 2 ** 28, {}, "i8_stream_16x64"), (16, 2 ** 29, {}, "i8_any_64x128"),
+    (2 ** 30, 256, {}, "i8_tile_256x256"), (524288, 2 ** 14, dict(groups=65536), "i8_any_64x128"),
+], ids=str)
+def test_plan_takes_a_larger_tile(M, N, kw, kernel, monkeypatch):
+    """A launch has fewer than 2^32 threads."""
+    monkeypatch.delenv("DG_FORCE_GROUPED", raising=False)
+    name, programs = _plan(dg.dg_gemm_scaled_describe(dg.make_scaled_desc(M, N, 32, **kw)))
+    assert name == kernel and 0 < programs * (256 if "any" in name else 512) < 2 ** 32
+
+
+def test_launches_past_the_limit_are_refused():
+    for M, N, kw in ((2 ** 31 - 1, 2 ** 20, {}), (2 ** 20, 2 ** 25, dict(groups=65536, ldb=32, stride_b=0))):
+        with pytest.raises(dg.DgError) as e:
+            dg.dg_gemm_scaled_describe(dg.make_scaled_desc(M, N, 32, **kw))
+        assert e.value.status == NO
