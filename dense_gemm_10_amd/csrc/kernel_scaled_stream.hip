@@ -77,14 +77,25 @@ __global__ __launch_bounds__(64 * KW) void scaled_stream_kernel(ScaledArgs a)
     };
 
     if (g.alpha != 0.0f) {
-        // A ring of D steps in registers, so that D steps' loads are under way
-        // while one is multiplied.  Loads past the last whole step repeat it
+        // A ring of D steps in registers, whose loads are under way while the
+        // step before is multiplied.  Loads past the last whole step repeat it
         // and are not used: with none left out, the compiler can count them.
+        // D = 2 only where few wavefronts fit a compute unit anyway: more
+        // registers cost wavefronts (13 rows, 16384 x 8192, 16 x 64: 30 us
+        // with two, 28.3 with one).
         const int32_t full = (int32_t)(g.K / SK);
         int32_t s = wave;
         if (s < full) {
             Step ring[D];
-            auto fetch = [&](Step &r, int32_t at) { load(r, (int64_t)(at < full ? at : full - 1) * SK); };
+            // Workgroups begin at different steps, so that those running at one
+            // time do not all read the same few k of rows a power of two
+            // apart (13 rows, 16384 x 8192: 28.3 us without, 26.4 with; 64
+            // rows, 4 groups, 4096 x 4096 18.9 and 17.2).
+            const int32_t turn = (int32_t)(t.col_tile * 5 % (uint32_t)full);
+            auto fetch = [&](Step &r, int32_t at) {
+                at = (at < full ? at : full - 1) + turn;
+                load(r, (int64_t)(at < full ? at : at - full) * SK);
+            };
 #pragma unroll
             for (int i = 0; i < D; ++i)
                 fetch(ring[i], s + i * KW);
@@ -157,10 +168,11 @@ hipError_t launch_scaled_stream(int32_t variant, const ScaledArgs &a, uint32_t p
 {
     switch (variant) {
     case 0: return launch<1, 1, 8, 2>(a, programs, s);
-    case 1: return launch<1, 2, 8, 2>(a, programs, s);
-    case 2: return launch<1, 4, 8, 2>(a, programs, s);
-    case 3: return launch<2, 2, 8, 2>(a, programs, s);
-    case 4: return launch<2, 4, 8, 2>(a, programs, s);
+    case 1: return launch<1, 2, 8, 1>(a, programs, s);
+    case 2: return launch<1, 2, 4, 2>(a, programs, s);
+    case 3: return launch<1, 4, 8, 1>(a, programs, s);
+    case 4: return launch<2, 2, 8, 1>(a, programs, s);
+    case 5: return launch<2, 4, 8, 1>(a, programs, s);
     default: return hipErrorInvalidValue;
     }
 }

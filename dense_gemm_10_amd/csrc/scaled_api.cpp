@@ -88,15 +88,16 @@ hipError_t tile_kernel(const ScaledArgs &a, uint32_t p, hipStream_t s) { return 
 
 const ScaledKernel kS16x16 = {"i8_stream_16x16", 16, 16, 512, true, stream_kernel<0>};
 const ScaledKernel kS16x32 = {"i8_stream_16x32", 16, 32, 512, true, stream_kernel<1>};
-const ScaledKernel kS16x64 = {"i8_stream_16x64", 16, 64, 512, true, stream_kernel<2>};
-const ScaledKernel kS32x32 = {"i8_stream_32x32", 32, 32, 512, true, stream_kernel<3>};
-const ScaledKernel kS32x64 = {"i8_stream_32x64", 32, 64, 512, true, stream_kernel<4>};
+const ScaledKernel kS16x32short = {"i8_stream_16x32_short", 16, 32, 256, true, stream_kernel<2>};
+const ScaledKernel kS16x64 = {"i8_stream_16x64", 16, 64, 512, true, stream_kernel<3>};
+const ScaledKernel kS32x32 = {"i8_stream_32x32", 32, 32, 512, true, stream_kernel<4>};
+const ScaledKernel kS32x64 = {"i8_stream_32x64", 32, 64, 512, true, stream_kernel<5>};
 const ScaledKernel kAny64 = {"i8_any_64x128", 64, 128, 256, true, tile_kernel<0>};
 const ScaledKernel kAny128 = {"i8_any_128x128", 128, 128, 256, true, tile_kernel<1>};
 const ScaledKernel kT128deep = {"i8_tile_128x128_deep", 128, 128, 512, false, tile_kernel<2>};
 const ScaledKernel kT128 = {"i8_tile_128x128", 128, 128, 512, false, tile_kernel<3>};
 const ScaledKernel kT256 = {"i8_tile_256x256", 256, 256, 512, false, tile_kernel<4>};
-const ScaledKernel *const kKernels[] = {&kS16x16, &kS16x32, &kS16x64, &kS32x32, &kS32x64,
+const ScaledKernel *const kKernels[] = {&kS16x16, &kS16x32short, &kS16x32, &kS16x64, &kS32x32, &kS32x64,
                                         &kAny64, &kAny128, &kT128deep, &kT128, &kT256};
 
 struct ScaledPlan {
@@ -129,17 +130,22 @@ double expected_tiles(const dg_scaled_desc *d, int64_t bm, int64_t bn)
 
 // The kernel for a problem, by the mean rows of a group (us, MI355X, int8 in,
 // bf16 out, B from memory; M x N x K):
-//   up to 16 (8 with groups), the 16-row streaming kernels, the widest that
-//     still makes enough workgroups: 1 x 4096 x 4096 6.1 on 16 columns, 7.7 on
-//     32, 11.2 on 64; 1 x 6000 x 4096 8.4, 7.7, 11.3; 16 x 8192 x 8192 20.4,
-//     17.6, 24.7; 13 x 16384 x 8192 36.3, 37.8, 30.1; 64 rows, 64 groups, 2048
-//     x 2048 32.2, 31.1, 30.3; 8 rows, 8 groups, 1024 x 1024 6.2, 6.0, 7.7;
+//   up to 16 (8 with groups), the 16-row streaming kernels.  16 columns where
+//     32 would make fewer than 160 workgroups (1 x 4096 x 4096 6.1 against
+//     7.7, and 11.2 on 64; 1 x 6000 x 4096 8.4 against 7.7); four wavefronts
+//     instead of eight on 32 for K up to 2048 (64 rows, 64 groups, 2048 x
+//     2048 25.2 against 28; 2048 x 1024 16.8 against 18.5; but 16 x 8192 x 8192
+//     16.3 against 15.8), 64 columns from 256 workgroups of them with one
+//     matrix and longer K (13 x 16384 x 8192 26.4 against 28.1, and 31.6 on
+//     16);
+//   one matrix, up to 32 rows: 16 x 32 while that is one workgroup per
+//     compute unit (32 x 4096 x 4096 9.3 against 11.3 on 32 x 32);
 //   then 32-row ones while they are one workgroup per compute unit: 64 x 4096 x
-//     4096 11.5 on 32 x 32, 15.5 on 32 x 64, 17.7 on 128 x 128; 64 x 8192 x
-//     4096 18.8, 16.1, 19.0; 128 x 8192 x 4096 33.0, 28.9, 20.2; groups of 9
+//     4096 11.4 on 32 x 32, 15.5 on 32 x 64, 17.7 on 128 x 128; 64 x 8192 x
+//     4096 18.8, 16.4, 19.0; 128 x 8192 x 4096 33.0, 28.9, 20.2; groups of 9
 //     to 16 rows 32 x 32 unless 128 x 128 tiles fill the chip twice (100 rows,
-//     8 groups, 4096 x 4096 33.3 against 35.8; 1024 rows, 64 groups, 2048 x
-//     2048 80 against 57.6, and 74 on 16 x 64);
+//     8 groups, 4096 x 4096 33 against 36; 1024 rows, 64 groups, 2048 x 2048
+//     80 against 57.6, and 74 on 16 x 64);
 //   128 x 128 with a ring of four stages, one workgroup per compute unit, up
 //     to 256 tiles (1024 x 4096 x 4096 21.3 against 27.2 with two stages and
 //     30.3 on 256 x 256), with two stages and two workgroups above (2000 rows,
@@ -151,8 +157,8 @@ double expected_tiles(const dg_scaled_desc *d, int64_t bm, int64_t bn)
 //     4096, 144 of them, 61 against 59).
 // Off the 16-byte grid, or with odd K: the same streaming kernels, then tiles
 // filled through registers, 64 x 128 until 128 x 128 ones fill the chip twice
-// (700 x 4097 x 1001 19 against 20, and 89 on 32 x 64; 2048 x 4096 x 4096 92
-// against 67).
+// (64 x 4097 x 1001 14 against 17 on 32 x 64; 700 x 4097 x 1001 19 against 20
+// on 128 x 128, and 89; 2048 x 4096 x 4096 92 against 67).
 const ScaledKernel *choose(const dg_scaled_desc *d, bool tile)
 {
     if (const char *want = getenv("DG_FORCE_GROUPED"))         // benchmarking and tests
@@ -163,10 +169,12 @@ const ScaledKernel *choose(const dg_scaled_desc *d, bool tile)
     const double mean = (double)d->M / (double)d->groups;
     if (mean <= (groups ? 8 : 16)) {
         const int64_t rt = row_tiles(d, 16);
-        return rt * ceil_div(d->N, 64) >= (groups ? 512 : 256) ? &kS16x64
-               : rt * ceil_div(d->N, 32) >= 160                ? &kS16x32
-                                                               : &kS16x16;
+        if (!groups && d->N >= 256 * 64 && d->K > 2048)
+            return &kS16x64;
+        return rt * ceil_div(d->N, 32) < 160 ? &kS16x16 : d->K > 2048 ? &kS16x32 : &kS16x32short;
     }
+    if (!groups && mean <= 32 && expected_tiles(d, 16, 32) <= 256)
+        return d->K > 2048 ? &kS16x32 : &kS16x32short;
     const double t128 = expected_tiles(d, 128, 128), t256 = expected_tiles(d, 256, 256);
     if (groups ? mean <= 16 && t128 <= 512 : expected_tiles(d, 32, 32) <= 256)
         return &kS32x32;
