@@ -143,21 +143,22 @@ __device__ __forceinline__ void copy_tail(char *dst, const char *src, int n, int
 
 constexpr int FEW_T = 256;
 
-// Few slots: maps and rows in one launch.  Workgroup b < S counts the slots
-// before slot b in the sorted order (all of them pass through it once),
-// writes its place and copies its token's row, whose first pieces are loaded
-// before the count.  Workgroup S writes the offsets and the end of order.
-template <typename I>
+// Few slots: maps and rows in one launch.  A workgroup has up to KB slots of
+// one token.  It counts the slots before each in the sorted order (all S of
+// them pass through it once), writes their places and copies the row there,
+// whose first pieces are loaded before the count.  The last workgroup writes
+// the offsets and the end of order.
+template <typename I, int KB>
 __global__ __launch_bounds__(FEW_T) void dispatch_few_kernel(DispatchArgs a)
 {
-    extern __shared__ int32_t count[];              // of the groups; workgroup S
-    __shared__ int32_t sums[FEW_T / 64];
+    extern __shared__ int32_t count[];              // of the groups; last workgroup
+    __shared__ int32_t sums[FEW_T / 64], parts[KB][FEW_T / 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int32_t S = a.slots, G = a.groups;
-    const int32_t b = (int32_t)blockIdx.x;
-    if (b < S) {
-        const int32_t e = slot_group<I>(a, (uint32_t)b);
-        const char *src = a.x + (int64_t)(b / a.top_k) * a.ldx;
+    if (blockIdx.x + 1 < gridDim.x) {
+        const uint32_t per = ((uint32_t)a.top_k + KB - 1) / KB;       // workgroups of a token
+        const int32_t t = (int32_t)(blockIdx.x / per), j0 = (int32_t)(blockIdx.x - t * per) * KB;
+        const char *src = a.x + (int64_t)t * a.ldx;
         constexpr int HELD = 2;
         Raw16 held[HELD];
 #pragma unroll
@@ -166,40 +167,66 @@ __global__ __launch_bounds__(FEW_T) void dispatch_few_kernel(DispatchArgs a)
             if (at + 16 <= a.width)
                 held[u] = load_raw16(src + at);
         }
-        int32_t n = 0;
-        for (int32_t s = tid; s < S; s += FEW_T) {
-            const int32_t v = slot_group<I>(a, (uint32_t)s);
-            n += v < e || (v == e && s < b);
+        const int32_t b = t * a.top_k + j0;     // its first slot
+        int32_t e[KB], n[KB];
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+            e[j] = j0 + j < a.top_k ? slot_group<I>(a, (uint32_t)(b + j)) : G;
+            n[j] = 0;
         }
-        n = wave_scan_add(n);
-        if (lane == 63)
-            sums[wave] = n;
+        constexpr int U = 4;                    // loads in flight
+        for (int32_t s0 = 0; s0 < S; s0 += U * FEW_T) {
+            int32_t v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int32_t s = s0 + u * FEW_T + tid;
+                v[u] = s < S ? slot_group<I>(a, (uint32_t)s) : G;      // before no slot of a group
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int32_t s = s0 + u * FEW_T + tid;
+#pragma unroll
+                for (int j = 0; j < KB; ++j)
+                    n[j] += v[u] < e[j] || (v[u] == e[j] && s < b + j);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+            const int32_t sum = wave_scan_add(n[j]);
+            if (lane == 63)
+                parts[j][wave] = sum;
+        }
         __syncthreads();
-        if (e >= G) {
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+            if (j0 + j >= a.top_k)
+                continue;
+            if (e[j] >= G) {
+                if (tid == 0)
+                    a.place[b + j] = -1;
+                continue;
+            }
+            int32_t p = 0;
+#pragma unroll
+            for (int w = 0; w < FEW_T / 64; ++w)
+                p += parts[j][w];
+            if (tid == 0) {
+                a.place[b + j] = p;
+                a.order[p] = b + j;
+            }
+            char *dst = a.rows + (int64_t)p * a.ldr;
+#pragma unroll
+            for (int u = 0; u < HELD; ++u) {
+                const int64_t at = (int64_t)(u * FEW_T + tid) * 16;
+                if (at + 16 <= a.width)
+                    store_raw16(dst + at, held[u]);
+            }
+            for (int64_t at = (int64_t)(HELD * FEW_T + tid) * 16; at + 16 <= a.width; at += FEW_T * 16)
+                store_raw16(dst + at, load_raw16(src + at));
+            const int64_t whole = a.width & ~(int64_t)15;
             if (tid == 0)
-                a.place[b] = -1;
-            return;
+                copy_tail(dst + whole, src + whole, (int)(a.width - whole), a.elem);
         }
-        int32_t p = 0;
-#pragma unroll
-        for (int w = 0; w < FEW_T / 64; ++w)
-            p += sums[w];
-        if (tid == 0) {
-            a.place[b] = p;
-            a.order[p] = b;
-        }
-        char *dst = a.rows + (int64_t)p * a.ldr;
-#pragma unroll
-        for (int u = 0; u < HELD; ++u) {
-            const int64_t at = (int64_t)(u * FEW_T + tid) * 16;
-            if (at + 16 <= a.width)
-                store_raw16(dst + at, held[u]);
-        }
-        for (int64_t at = (int64_t)(HELD * FEW_T + tid) * 16; at + 16 <= a.width; at += FEW_T * 16)
-            store_raw16(dst + at, load_raw16(src + at));
-        const int64_t whole = a.width & ~(int64_t)15;
-        if (tid == 0)
-            copy_tail(dst + whole, src + whole, (int)(a.width - whole), a.elem);
         return;
     }
     for (int i = tid; i < G; i += FEW_T)
@@ -273,6 +300,17 @@ __global__ __launch_bounds__(SPREAD_T) void spread_kernel(SpreadArgs a)
     }
 }
 
+template <int KB>
+void launch_few(const DispatchArgs &a, hipStream_t s)
+{
+    const dim3 grid((unsigned)(a.slots / a.top_k * ((a.top_k + KB - 1) / KB)) + 1);
+    const size_t lds = (size_t)a.groups * 4;
+    if (a.index_bits == 64)
+        hipLaunchKernelGGL((dispatch_few_kernel<int64_t, KB>), grid, dim3(FEW_T), lds, s, a);
+    else
+        hipLaunchKernelGGL((dispatch_few_kernel<int32_t, KB>), grid, dim3(FEW_T), lds, s, a);
+}
+
 } // namespace
 
 hipError_t launch_dispatch_sort(const DispatchArgs &a, hipStream_t s)
@@ -294,12 +332,13 @@ hipError_t launch_dispatch_sort(const DispatchArgs &a, hipStream_t s)
 
 hipError_t launch_dispatch_few(const DispatchArgs &a, hipStream_t s)
 {
-    const dim3 grid((unsigned)a.slots + 1);
-    const size_t lds = (size_t)a.groups * 4;
-    if (a.index_bits == 64)
-        hipLaunchKernelGGL(dispatch_few_kernel<int64_t>, grid, dim3(FEW_T), lds, s, a);
+    // two slots a workgroup from 1024 on, where the counting bounds it (1024
+    // slots, 2 a token, 2048 bf16: 4.4 us with one, 4.6 with two; 2048 slots
+    // 7.4 and 6.5)
+    if (a.top_k == 1 || a.slots <= 1024)
+        launch_few<1>(a, s);
     else
-        hipLaunchKernelGGL(dispatch_few_kernel<int32_t>, grid, dim3(FEW_T), lds, s, a);
+        launch_few<2>(a, s);
     return hipGetLastError();
 }
 

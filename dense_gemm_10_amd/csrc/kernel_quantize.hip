@@ -1,88 +1,12 @@
-// 8-bit codes and scales of rows.
-//
-// One workgroup per token: the row's largest absolute value by an integer
-// maximum of the bits below the sign (a NaN is the largest, an infinity the
-// next, so neither is lost), then the codes.  A row of up to 8 CHUNKS x
-// 256 elements stays in registers, so x is read once.
-//
-// The code is the nearest integer to 127 x / max, ties to even, from the
-// exact quotient: with both scaled by a power of two so that max is in
-// [1, 2), x * (127 / max) in fp32 is off by less than 127 * 3 * 2^-24 <
-// 3e-5, so the nearest integer is right unless the rest comes within 1e-4 of
-// a half; then the sign of 127 x - (q +- 1/2) max decides, exact in fp64.
-#include "grouped.hpp"
-#include "tokens.hpp"
+// 8-bit codes and scales of rows (codes.hpp): one workgroup per token; a row of
+// up to 8 CHUNKS x 256 elements stays in registers, so x is read once.
+#include "codes.hpp"
 
 namespace dg {
 
 namespace {
 
 constexpr int QT = 256;
-
-template <int T>
-__device__ __forceinline__ uint32_t raw_abs_max(const Raw8<T> &r)      // fp32: bits; else 16 bits
-{
-    uint32_t m = 0;
-    if constexpr (T == DT_F32) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            m = max(m, r.w[i] & 0x7fffffffu);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            m = max(m, r.w[i] & 0x7fffu);
-            m = max(m, (r.w[i] >> 16) & 0x7fffu);
-        }
-    }
-    return m;
-}
-
-__device__ __forceinline__ uint32_t wave_max(uint32_t v)               // v below 2^31
-{
-    return (uint32_t)__builtin_amdgcn_readlane(wave_scan_max((int32_t)v), 63);
-}
-
-struct RowScale {
-    float top, inv;      // of the row scaled by 2^shift: in [1, 2), and 127 / top
-    int shift;
-    bool zero;           // every code is 0
-};
-
-// The code of x from the exact quotient.
-__device__ __forceinline__ float exact_code(float xs, float q, float top)
-{
-    const double r2 = 2.0 * (127.0 * (double)xs - (double)q * (double)top);   // exact
-    const double t = (double)top;
-    const bool odd = ((int)q & 1) != 0;
-    if (r2 > t || (r2 == t && odd))
-        return q + 1.0f;
-    if (r2 < -t || (r2 == -t && odd))
-        return q - 1.0f;
-    return q;
-}
-
-// Eight codes, packed.
-template <int T>
-__device__ __forceinline__ uint2 codes(const Raw8<T> &r, const RowScale &s)
-{
-    float q[8], worst = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float v = __builtin_amdgcn_ldexpf(raw_value<T>(r, e), s.shift) * s.inv;
-        q[e] = __builtin_rintf(v);
-        worst = fmaxf(worst, fabsf(v - q[e]));
-    }
-    if (worst > 0.4999f) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            q[e] = exact_code(__builtin_amdgcn_ldexpf(raw_value<T>(r, e), s.shift), q[e], s.top);
-    }
-    uint32_t b[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        b[e] = s.zero ? 0u : (uint32_t)(int32_t)q[e] & 255u;
-    return make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
-}
 
 __device__ __forceinline__ void store_codes(int8_t *p, uint2 c, int n)
 {
@@ -133,15 +57,7 @@ __global__ __launch_bounds__(QT) void quantize_kernel(QuantizeArgs a)
 #pragma unroll
         for (int w = 0; w < QT / 64; ++w)
             m = max(m, tops[turn][w]);
-        const float top = T == DT_F32 ? __uint_as_float(m)
-                                      : half_to_f32<T == DT_F32 ? DT_BF16 : T>((uint16_t)m);
-        const bool finite = top < __builtin_inff();            // false for NaN
-        RowScale s;
-        s.zero = !finite || top == 0.0f;
-        s.shift = s.zero ? 0 : 1 - __builtin_amdgcn_frexp_expf(top);
-        s.top = s.zero ? 1.0f : __builtin_amdgcn_ldexpf(top, s.shift);
-        s.inv = 127.0f / s.top;
-        const float scale = finite ? (float)((double)top / 127.0) : __builtin_nanf("");
+        const RowScale s = row_scale<T>(m);
         const int32_t copies = a.place ? a.top_k : 1;
         auto put = [&](int64_t c, uint2 q) {
             for (int32_t j = 0; j < copies; ++j) {
@@ -168,7 +84,7 @@ __global__ __launch_bounds__(QT) void quantize_kernel(QuantizeArgs a)
         for (int32_t j = tid; j < copies; j += QT) {
             const int64_t p = a.place ? a.place[t * a.top_k + j] : t;
             if (!a.place || (p >= 0 && p < a.limit))
-                a.scales[p] = scale;
+                a.scales[p] = s.scale;
         }
     }
 }

@@ -15,7 +15,15 @@ struct ScaledArgs {
     int32_t scale_type;        // of scale_b
     int64_t stride_s, stride_bias;   // elements
     uint32_t tiles_n;
+    // few rows whose codes the product makes itself: their type and leading
+    // dimension in bytes
+    const char *x;
+    int64_t ldx;
+    int32_t x_type;
 };
+
+constexpr int kFewRows = 4;
+constexpr int64_t kFewElements = 8192;      // of all of them
 
 // Tile of program `pid` of one matrix of `rows` rows: as find_group_tile of
 // one group, without the lookup.
@@ -103,6 +111,8 @@ __device__ __forceinline__ Bytes16 load_masked16(const int8_t *row, int64_t k, i
 
 // Launchers; each returns hipSuccess or the launch error.
 hipError_t launch_scaled_stream(int32_t variant, const ScaledArgs &a, uint32_t programs, hipStream_t s);
+// of x, up to kFewRows rows and kFewElements
+hipError_t launch_scaled_few(int32_t variant, const ScaledArgs &a, uint32_t programs, hipStream_t s);
 hipError_t launch_scaled_tile(int32_t variant, const ScaledArgs &a, uint32_t programs, hipStream_t s);
 
 } // namespace dg

@@ -40,6 +40,17 @@ struct Spans {
 bool is_noop(const dg_scaled_desc *d) { return d->groups == 0 || d->N == 0 || d->M == 0; }
 bool reads_ab(const dg_scaled_desc *d) { return d->alpha != 0.0f && d->K > 0; }
 
+// Few float rows, whose codes every workgroup of the product makes itself: no
+// workspace and no second launch (a 1 x 4096 x 4096 call takes the host 7.0 us
+// instead of 11.8 and the GPU, in a graph, 8.3 instead of 10.0; of more elements
+// the codes cost the workgroups more than they save: 4 x 16384 x 8192 35.8
+// against 31.8).
+bool few_rows(const dg_scaled_desc *d)
+{
+    return d->a_type != DG_I8 && d->groups == 1 && d->M <= DG_SCALED_FEW_ROWS && d->M * d->K <= DG_SCALED_FEW_ELEMENTS;
+}
+static_assert(DG_SCALED_FEW_ROWS == kFewRows && DG_SCALED_FEW_ELEMENTS == kFewElements, "as the kernel has it");
+
 // Leading dimension of the codes made of a float A: rows on 16 bytes.
 int64_t codes_ld(const dg_scaled_desc *d) { return d->K > 0 ? ceil_div(d->K, 16) * 16 : 16; }
 
@@ -67,8 +78,9 @@ dg_status validate(const dg_scaled_desc *d, Spans *s)
         bytes_of(d->groups, d->stride_s, 1, d->N, n_ld, elem_size(d->scale_type), &s->sb) &&
         bytes_of(1, 0, d->M, d->N, d->ldc, elem_size(d->c_type), &s->c) &&
         (!d->bias || bytes_of(d->groups, d->stride_bias, 1, d->N, n_ld, elem_size(d->bias_type), &s->bias));
-    s->codes = d->a_type == DG_I8 ? 0 : d->M * codes_ld(d);          // below 2^31 * 2^18
-    s->workspace = d->a_type == DG_I8 ? 0 : s->codes + s->sa;
+    const bool made = d->a_type != DG_I8 && !few_rows(d);
+    s->codes = made ? d->M * codes_ld(d) : 0;                        // below 2^31 * 2^18
+    s->workspace = made ? s->codes + s->sa : 0;
     return ok ? DG_SUCCESS : DG_ERROR_INVALID_VALUE;
 }
 
@@ -79,6 +91,7 @@ struct ScaledKernel {
     int32_t bm, bn, threads;
     bool any_alignment;
     ScaledLaunch launch;
+    ScaledLaunch few;          // of few float rows, whose codes it makes itself
 };
 
 template <int V>
@@ -86,17 +99,20 @@ hipError_t stream_kernel(const ScaledArgs &a, uint32_t p, hipStream_t s) { retur
 template <int V>
 hipError_t tile_kernel(const ScaledArgs &a, uint32_t p, hipStream_t s) { return launch_scaled_tile(V, a, p, s); }
 
-const ScaledKernel kS16x16 = {"i8_stream_16x16", 16, 16, 512, true, stream_kernel<0>};
-const ScaledKernel kS16x32 = {"i8_stream_16x32", 16, 32, 512, true, stream_kernel<1>};
-const ScaledKernel kS16x32short = {"i8_stream_16x32_short", 16, 32, 256, true, stream_kernel<2>};
-const ScaledKernel kS16x64 = {"i8_stream_16x64", 16, 64, 512, true, stream_kernel<3>};
-const ScaledKernel kS32x32 = {"i8_stream_32x32", 32, 32, 512, true, stream_kernel<4>};
-const ScaledKernel kS32x64 = {"i8_stream_32x64", 32, 64, 512, true, stream_kernel<5>};
-const ScaledKernel kAny64 = {"i8_any_64x128", 64, 128, 256, true, tile_kernel<0>};
-const ScaledKernel kAny128 = {"i8_any_128x128", 128, 128, 256, true, tile_kernel<1>};
-const ScaledKernel kT128deep = {"i8_tile_128x128_deep", 128, 128, 512, false, tile_kernel<2>};
-const ScaledKernel kT128 = {"i8_tile_128x128", 128, 128, 512, false, tile_kernel<3>};
-const ScaledKernel kT256 = {"i8_tile_256x256", 256, 256, 512, false, tile_kernel<4>};
+template <int V>
+hipError_t few_kernel(const ScaledArgs &a, uint32_t p, hipStream_t s) { return launch_scaled_few(V, a, p, s); }
+
+const ScaledKernel kS16x16 = {"i8_stream_16x16", 16, 16, 512, true, stream_kernel<0>, few_kernel<0>};
+const ScaledKernel kS16x32 = {"i8_stream_16x32", 16, 32, 512, true, stream_kernel<1>, few_kernel<1>};
+const ScaledKernel kS16x32short = {"i8_stream_16x32_short", 16, 32, 256, true, stream_kernel<2>, nullptr};
+const ScaledKernel kS16x64 = {"i8_stream_16x64", 16, 64, 512, true, stream_kernel<3>, few_kernel<2>};
+const ScaledKernel kS32x32 = {"i8_stream_32x32", 32, 32, 512, true, stream_kernel<4>, nullptr};
+const ScaledKernel kS32x64 = {"i8_stream_32x64", 32, 64, 512, true, stream_kernel<5>, nullptr};
+const ScaledKernel kAny64 = {"i8_any_64x128", 64, 128, 256, true, tile_kernel<0>, nullptr};
+const ScaledKernel kAny128 = {"i8_any_128x128", 128, 128, 256, true, tile_kernel<1>, nullptr};
+const ScaledKernel kT128deep = {"i8_tile_128x128_deep", 128, 128, 512, false, tile_kernel<2>, nullptr};
+const ScaledKernel kT128 = {"i8_tile_128x128", 128, 128, 512, false, tile_kernel<3>, nullptr};
+const ScaledKernel kT256 = {"i8_tile_256x256", 256, 256, 512, false, tile_kernel<4>, nullptr};
 const ScaledKernel *const kKernels[] = {&kS16x16, &kS16x32short, &kS16x32, &kS16x64, &kS32x32, &kS32x64,
                                         &kAny64, &kAny128, &kT128deep, &kT128, &kT256};
 
@@ -161,6 +177,13 @@ double expected_tiles(const dg_scaled_desc *d, int64_t bm, int64_t bn)
 // on 128 x 128, and 89; 2048 x 4096 x 4096 92 against 67).
 const ScaledKernel *choose(const dg_scaled_desc *d, bool tile)
 {
+    if (few_rows(d) && reads_ab(d)) {
+        const char *want = getenv("DG_FORCE_GROUPED");
+        for (const ScaledKernel *k : {&kS16x16, &kS16x32, &kS16x64})
+            if (want && !strcmp(want, k->name))
+                return k;
+        return d->N >= 256 * 64 && d->K > 2048 ? &kS16x64 : ceil_div(d->N, 32) < 160 ? &kS16x16 : &kS16x32;
+    }
     if (const char *want = getenv("DG_FORCE_GROUPED"))         // benchmarking and tests
         for (const ScaledKernel *k : kKernels)
             if (!strcmp(want, k->name) && (k->any_alignment || tile))
@@ -192,7 +215,7 @@ dg_status make_plan(const dg_scaled_desc *d, const void *A, const void *B, Scale
     const bool tile = tile_ok(d, A, B);
     auto fits = [&](const ScaledKernel &k) {
         int64_t n;
-        if ((!k.any_alignment && !tile) || !mul_ok(row_tiles(d, k.bm), ceil_div(d->N, k.bn), &n) ||
+        if ((!k.any_alignment && !tile) || (few_rows(d) && reads_ab(d) && !k.few) || !mul_ok(row_tiles(d, k.bm), ceil_div(d->N, k.bn), &n) ||
             n > (int64_t)UINT32_MAX / k.threads - 128)      // launch_mixed adds 128
             return false;
         p->programs = (uint32_t)n;
@@ -230,7 +253,7 @@ dg_status dg_gemm_scaled(const dg_scaled_desc *d, const void *A, const float *sc
     dg_status st = validate(d, &sp);
     if (st != DG_SUCCESS)
         return st;
-    const bool reads = reads_ab(d), make = d->a_type != DG_I8 && reads;
+    const bool reads = reads_ab(d), few = few_rows(d) && reads, make = d->a_type != DG_I8 && reads && !few;
     if ((!offsets && d->groups > 1) || (d->a_type != DG_I8 && scale_a))
         return DG_ERROR_INVALID_VALUE;
     if (is_noop(d))
@@ -299,7 +322,13 @@ dg_status dg_gemm_scaled(const dg_scaled_desc *d, const void *A, const float *sc
         if (launch_quantize(q, (hipStream_t)stream) != hipSuccess)
             return DG_ERROR_LAUNCH;
     }
-    return p.kernel->launch(a, p.programs, (hipStream_t)stream) == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
+    if (few) {
+        a.x = (const char *)A;
+        a.ldx = d->lda * a_bytes(d);
+        a.x_type = d->a_type;
+    }
+    const hipError_t err = (few ? p.kernel->few : p.kernel->launch)(a, p.programs, (hipStream_t)stream);
+    return err == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
 }
 
 dg_status dg_gemm_scaled_describe(const dg_scaled_desc *d, char *buf, size_t len)

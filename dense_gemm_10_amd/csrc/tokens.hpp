@@ -2,7 +2,7 @@
 // arguments and launchers (kernel_dispatch.hip, kernel_combine.hip,
 // kernel_quantize.hip; host side in tokens_api.cpp).
 #pragma once
-#include "common.hpp"
+#include "grouped.hpp"
 
 namespace dg {
 
@@ -66,7 +66,9 @@ hipError_t launch_combine(const CombineArgs &a, hipStream_t s);
 hipError_t launch_combine_grad(const CombineArgs &a, hipStream_t s);
 hipError_t launch_quantize(const QuantizeArgs &a, hipStream_t s);
 
-constexpr int32_t kDispatchFewSlots = 1024;
+// 4096 slots, 2 a token, 4096 bf16: 14.8 us against 7.3 + 9.8; 6000 slots 19.8
+// against 7.6 + 7.2
+constexpr int32_t kDispatchFewSlots = 4096;
 
 // ---- eight elements of a row -------------------------------------------------
 // Rows start on any element, so 16 bytes go by loads and stores that need no

@@ -13,6 +13,7 @@ from . import DG_F32, DG_SUCCESS, DgError, _ACT, _DTYPE, _enum, _load
 from .grouped import _bias, _check_offsets, _code, _launch, _output, _row_ld, _same_device
 
 DG_I8 = 3
+DG_SCALED_FEW_ROWS, DG_SCALED_FEW_ELEMENTS = 4, 8192
 _A_TYPE = dict(_DTYPE, i8=DG_I8)
 _i32, _i64, _f32, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
 
@@ -144,7 +145,7 @@ def gemm_scaled(A, B, scale_a=None, scale_b=None, C=None, *, offsets=None, alpha
     C = _output(C, (M, N), out_dtype or (None if own or C is not None else torch.bfloat16), A, beta)
     _same_device(device, B=B, C=C, offsets=offsets, bias=bias, scale_a=scale_a, scale_b=scale_b)
     bias_ptr, bias_type, stride_bias = _bias(bias, groups, N, grouped)
-    if own and M and K:
+    if own and K and M and (M > DG_SCALED_FEW_ROWS or M * K > DG_SCALED_FEW_ELEMENTS or groups > 1):
         ws_bytes = M * (((K + 15) & -16) + 4)
         ws = torch.empty(ws_bytes, dtype=int8, device=A.device)
     desc = _pack(_SIZE, _code(A) if own else DG_I8, _code(C), sb_type, bias_type, _enum(_ACT, act), groups, M, N, K,

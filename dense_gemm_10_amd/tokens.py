@@ -139,40 +139,57 @@ def _torch():
     return sys.modules["torch"]           # a tensor was passed: it is imported
 
 
+def _ld(t, rows, cols, name):
+    """Leading dimension of a row-major 2-D tensor."""
+    return cols or 1 if t.is_contiguous() else _row_ld(rows, cols, *t.stride(), name)
+
+
 def _matrix(t, name):
     """(rows, columns, leading dimension) of a row-major 2-D tensor."""
-    if t.dim() != 2:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, two dimensions are wanted")
-    r, c = t.shape
-    return r, c, _row_ld(r, c, *t.stride(), name)
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: shape {tuple(shape)}, two dimensions are wanted")
+    r, c = shape
+    return r, c, _ld(t, r, c, name)
 
 
 def _check_place(place):
-    if place.dtype != _torch().int32 or place.dim() != 2 or not place.is_contiguous():
+    shape = place.shape
+    if place.dtype != _torch().int32 or len(shape) != 2 or not place.is_contiguous():
         raise ValueError("place: a contiguous int32 tensor (tokens, top_k) is wanted")
-    return place.shape
+    return shape
+
+
+def _on_device(device, **tensors):
+    """Raises unless all of them are on the GPU `device`."""
+    if device < 0:
+        _same_device(device)
+    for t in tensors.values():
+        if t is not None and t.get_device() != device:
+            _same_device(device, **tensors)
 
 
 def _result(t, shape, dtype, like, name):
     """t checked, or a new tensor."""
     if t is None:
         return _torch().empty(shape, dtype=dtype, device=like.device)
-    if tuple(t.shape) != tuple(shape) or (dtype is not None and t.dtype != dtype):
+    if t.shape != shape or (dtype is not None and t.dtype != dtype):
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, {dtype} {tuple(shape)} is wanted")
     return t
 
 
 def _maps(index, groups):
     torch = _torch()
-    if index.dim() != 2 or index.dtype not in (torch.int32, torch.int64):
+    shape, dtype = index.shape, index.dtype
+    if len(shape) != 2 or (dtype != torch.int64 and dtype != torch.int32):
         raise ValueError("index: an int32 or int64 tensor (tokens, top_k) is wanted")
-    tokens, top_k = index.shape
-    ld = _row_ld(tokens, top_k, *index.stride(), "index")
+    tokens, top_k = shape
     if groups < 0:
         raise ValueError(f"groups {groups}")
-    new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=index.device)
-    return (tokens, top_k, ld, 64 if index.dtype == torch.int64 else 32, new(groups + 1),
-            new(tokens * top_k), new(tokens, top_k))
+    ld = _ld(index, tokens, top_k, "index")
+    empty, i32, where = torch.empty, torch.int32, index.device
+    return (tokens, top_k, ld, 64 if dtype == torch.int64 else 32, empty(groups + 1, dtype=i32, device=where),
+            empty(tokens * top_k, dtype=i32, device=where), empty(shape, dtype=i32, device=where))
 
 
 def sort_tokens(index, groups, *, stream=None):
@@ -203,9 +220,9 @@ def dispatch_tokens(x, index, groups, *, out=None, stream=None):
         raise ValueError(f"x has {n} rows, index {tokens}")
     rows = _result(out, (tokens * top_k, width), x.dtype, x, "out")
     device = x.get_device()
-    _same_device(device, index=index, out=rows)
+    _on_device(device, index=index, out=rows)
     desc = _pack_dispatch(_DISPATCH_SIZE, _code(x), bits, tokens, top_k, groups, tokens * top_k, width, ld, ldx,
-                          _row_ld(tokens * top_k, width, *rows.stride(), "out"))
+                          _ld(rows, tokens * top_k, width, "out"))
     _launch(_fast("dg_dispatch"), "dg_dispatch", device, stream, desc, index.data_ptr(), x.data_ptr(),
             offsets.data_ptr(), order.data_ptr(), place.data_ptr(), rows.data_ptr())
     return rows, offsets, order, place
@@ -222,9 +239,9 @@ def spread_tokens(x, place, *, out=None, stream=None):
         raise ValueError(f"x has {n} rows, place {tokens}")
     rows = _result(out, (tokens * top_k if out is None else out.shape[0], width), x.dtype, x, "out")
     device = x.get_device()
-    _same_device(device, place=place, out=rows)
+    _on_device(device, place=place, out=rows)
     desc = _pack_dispatch(_DISPATCH_SIZE, _code(x), 32, tokens, top_k, 0, rows.shape[0], width, max(1, top_k), ldx,
-                          _row_ld(rows.shape[0], width, *rows.stride(), "out"))
+                          _ld(rows, rows.shape[0], width, "out"))
     _launch(_fast("dg_spread"), "dg_spread", device, stream, desc, place.data_ptr(), x.data_ptr(),
             rows.data_ptr())
     return rows
@@ -234,9 +251,9 @@ def _weights(weights, shape):
     """(address, type, leading dimension)."""
     if weights is None:
         return None, DG_F32, max(1, shape[1])
-    if tuple(weights.shape) != tuple(shape):
+    if weights.shape != shape:
         raise ValueError(f"weights: shape {tuple(weights.shape)}, {tuple(shape)} is wanted")
-    return weights.data_ptr(), _code(weights), _row_ld(*shape, *weights.stride(), "weights")
+    return weights.data_ptr(), _code(weights), _ld(weights, *shape, "weights")
 
 
 def combine_tokens(z, place, weights=None, y=None, *, beta=0.0, out_dtype=None, stream=None):
@@ -253,10 +270,10 @@ def combine_tokens(z, place, weights=None, y=None, *, beta=0.0, out_dtype=None, 
         raise ValueError("beta != 0 needs an input y")
     y = _result(y, (tokens, width), out_dtype or (z.dtype if y is None else None), z, "y")
     device = z.get_device()
-    _same_device(device, place=place, weights=weights, y=y)
+    _on_device(device, place=place, weights=weights, y=y)
     w, wt, ldw = _weights(weights, (tokens, top_k))
     desc = _pack_combine(_COMBINE_SIZE, _code(z), _code(y), wt, tokens, top_k, rows, width, ldz, ldz,
-                         _row_ld(tokens, width, *y.stride(), "y"), ldw, beta)
+                         _ld(y, tokens, width, "y"), ldw, beta)
     _launch(_fast("dg_combine"), "dg_combine", device, stream, desc, z.data_ptr(), place.data_ptr(), w,
             y.data_ptr())
     return y
@@ -279,9 +296,9 @@ def combine_tokens_grad(dy, z, place, weights, *, dz=None, stream=None):
     dz = _result(dz, (rows, width), z.dtype, z, "dz")
     dw = _torch().empty((tokens, top_k), dtype=weights.dtype, device=z.device)
     device = z.get_device()
-    _same_device(device, dy=dy, place=place, weights=weights, dz=dz)
+    _on_device(device, dy=dy, place=place, weights=weights, dz=dz)
     desc = _pack_combine(_COMBINE_SIZE, _code(z), _code(dy), wt, tokens, top_k, rows, width, ldz,
-                         _row_ld(rows, width, *dz.stride(), "dz"), ldy, ldw, 0.0)
+                         _ld(dz, rows, width, "dz"), ldy, ldw, 0.0)
     _launch(_fast("dg_combine_grad"), "dg_combine_grad", device, stream, desc, dy.data_ptr(), z.data_ptr(),
             place.data_ptr(), w, dz.data_ptr(), dw.data_ptr())
     return dz, dw
@@ -312,9 +329,9 @@ def quantize_rows(x, place=None, q=None, scales=None, *, stream=None):
     if not scales.is_contiguous():
         raise ValueError("scales: a contiguous tensor is wanted")
     device = x.get_device()
-    _same_device(device, place=place, q=q, scales=scales)
+    _on_device(device, place=place, q=q, scales=scales)
     desc = _pack_quantize(_QUANTIZE_SIZE, _code(x), tokens, top_k, rows, width, ldx,
-                          _row_ld(rows, width, *q.stride(), "q"))
+                          _ld(q, rows, width, "q"))
     _launch(_fast("dg_quantize"), "dg_quantize", device, stream, desc, x.data_ptr(),
             None if place is None else place.data_ptr(), q.data_ptr(), scales.data_ptr())
     return q, scales

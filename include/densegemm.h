@@ -525,7 +525,7 @@ dg_status dg_quantize(const dg_quantize_desc *d, const void *x, const int32_t *p
  * (half a step of 24 bits) and multiplied by scale_a, scale_b and alpha in
  * that order.  scale_a (fp32) or scale_b NULL: ones.
  * a_type F32, BF16 or F16: A's rows are turned into codes and scales first,
- * as by dg_quantize, in the workspace; scale_a must be NULL.
+ * as by dg_quantize, in the workspace if there is one; scale_a must be NULL.
  * With offsets, row i of A and C uses the B of the group that holds it, B + e
  * * stride_b, scale_b + e * stride_s, bias + e * stride_bias; the offsets as
  * in dg_gemm_grouped with M in the place of rows, and rows of no group left
@@ -552,7 +552,11 @@ typedef struct dg_scaled_desc {
     const void *bias;
 } dg_scaled_desc;
 
-/* Device bytes of workspace of dg_gemm_scaled: 0 for a_type DG_I8. */
+/* Device bytes of workspace of dg_gemm_scaled: 0 for a_type DG_I8, and for up
+ * to DG_SCALED_FEW_ROWS rows of up to DG_SCALED_FEW_ELEMENTS elements together
+ * with groups 1. */
+#define DG_SCALED_FEW_ROWS 4
+#define DG_SCALED_FEW_ELEMENTS 8192
 dg_status dg_gemm_scaled_workspace_size(const dg_scaled_desc *d, size_t *bytes);
 
 /* Enqueue the product on `stream`; may be captured.  workspace: 16-byte

@@ -156,6 +156,38 @@ def test_float_operand(M, K, dtype):
     check(got.cpu(), ref, tol)
 
 
+@pytest.mark.parametrize("kernel", ["i8_stream_16x16", "i8_stream_16x32", "i8_stream_16x64"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_few_float_rows_need_no_workspace(dtype, kernel, monkeypatch):
+    """Up to four rows and 8192 elements: one launch, the same bits as quantize_rows and
+    the product, whatever K, alignment and offsets of one group."""
+    monkeypatch.setenv("DG_FORCE_GROUPED", kernel)
+    gen = torch.Generator().manual_seed(21)
+    for M, K, N, pad in ((1, 4096, 48, 0), (1, 8192, 33, 0), (3, 1001, 70, 1), (4, 7, 100, 0), (4, 128, 20, 5),
+                         (1, 130, 64, 0), (2, 4095, 17, 2), (4, 2040, 300, 8), (4, 2048, 30, 0)):
+        desc = dg.make_scaled_desc(M, N, K, a_type=dtype)
+        assert dg.dg_gemm_scaled_workspace_size(desc) == 0
+        assert f"kernel={kernel} " in dg.dg_gemm_scaled_describe(desc)
+        x = torch.zeros(M, K + pad)
+        x[:, :K] = torch.randn(M, K, generator=gen)
+        if M > 2:
+            x[1], x[2, K // 2] = 0, float("nan")
+        x = x.to(DT[dtype]).cuda()[:, :K]
+        B, sb = _padded(_i8(gen, N, K), pad), torch.rand(N, generator=gen).cuda() / 100
+        bias = torch.randn(N, generator=gen).cuda()
+        q, s = dg.quantize_rows(x)
+        for kw in ({}, dict(act="gelu_erf", bias=bias, alpha=0.5), dict(out_dtype=torch.float32)):
+            got = dg.gemm_scaled(x, B, None, sb, **kw)
+            want = dg.gemm_scaled(q, B, s, sb, **dict(dict(out_dtype=DT[dtype]), **kw))
+            assert same_bits(got.nan_to_num(nan=5.0), want.nan_to_num(nan=5.0)), (M, K)
+        for lo, hi in ((0, M), (1, M), (1, M - 1), (0, 0)):
+            off = torch.tensor([lo, hi], dtype=torch.int32).cuda()
+            a, b = torch.full((2, M, N), 9.0, device="cuda")
+            dg.gemm_scaled(x, B[None], None, sb[None], a, offsets=off)
+            dg.gemm_scaled(q, B[None], s, sb[None], b, offsets=off)
+            assert same_bits(a.nan_to_num(nan=5.0), b.nan_to_num(nan=5.0)), (M, K, lo, hi)
+
+
 def test_largest_sums():
     K = 131071
     for kernel_rows in (1, 300):

@@ -84,6 +84,10 @@ def test_workspace_of_a_float_operand():
     assert need == 5 * 80 + 5 * 4
     assert dg.dg_gemm_scaled_workspace_size(_d()) == 0
     assert dg.dg_gemm_scaled_workspace_size(_d(a_type="bf16", alpha=0.0)) == 0
+    for kw, none in ((dict(M=4, K=2048), True), (dict(M=5, K=1024), False), (dict(M=4, K=2049), False),
+                     (dict(M=1, K=8192), True), (dict(M=1, K=8193), False),
+                     (dict(M=1, groups=2), False)):
+        assert (dg.dg_gemm_scaled_workspace_size(_d(**dict(dict(a_type="f16"), **kw))) == 0) == none, kw
     assert _run(d, sa=PSA) == BAD
     assert _run(d, sa=None) == SHORT and _run(d, sa=None, ws=PW, n=need - 1) == SHORT
     assert _run(d, sa=None, A=PA + 1, ws=PW, n=need) == BAD
@@ -140,6 +144,8 @@ def _plan(text):
     (64, 8192, 4096, {}, "i8_stream_32x64"), (128, 8192, 4096, {}, "i8_tile_128x128_deep"),
     (1024, 4096, 4096, {}, "i8_tile_128x128_deep"), (2048, 2560, 1024, {}, "i8_tile_128x128"),
     (2048, 4096, 4096, {}, "i8_tile_256x256"),
+    (1, 4096, 4096, dict(a_type="bf16"), "i8_stream_16x16"), (1, 8192, 2048, dict(a_type="bf16"), "i8_stream_16x32"),
+    (1, 16384, 8192, dict(a_type="f32"), "i8_stream_16x64"), (5, 16384, 2048, dict(a_type="f32"), "i8_stream_16x32_short"),
     (8, 1024, 1024, dict(groups=8), "i8_stream_16x32_short"), (64, 2048, 2048, dict(groups=64), "i8_stream_16x32_short"), (32, 4096, 4096, {}, "i8_stream_16x32"),
     (32, 4096, 1000, {}, "i8_stream_16x32_short"), (32, 8192, 4096, {}, "i8_stream_32x32"),
     (100, 4096, 4096, dict(groups=8), "i8_stream_32x32"), (1024, 2048, 2048, dict(groups=64), "i8_tile_128x128"),
@@ -158,7 +164,7 @@ def test_kernel_of_a_problem(M, N, K, kw, kernel, monkeypatch):
 
 
 @pytest.mark.parametrize("M,N,kw,kernel", [
-    (16, 2 ** 28, {}, "i8_stream_16x32_short"), (16, 2 ** 30, {}, "i8_any_64x128"),
+    (16, 2 ** 28, {}, "i8_stream_16x32_short"), (16, 2 ** 30, {}, "i8_any_64x128"), (1, 2 ** 28, dict(a_type="bf16"), "i8_stream_16x64"),
     (2 ** 30, 256, {}, "i8_tile_256x256"), (524288, 2 ** 14, dict(groups=65536), "i8_any_64x128"),
 ], ids=str)
 def test_plan_takes_a_larger_tile(M, N, kw, kernel, monkeypatch):
@@ -169,7 +175,7 @@ def test_plan_takes_a_larger_tile(M, N, kw, kernel, monkeypatch):
 
 
 def test_launches_past_the_limit_are_refused():
-    for M, N, kw in ((2 ** 31 - 1, 2 ** 20, {}), (2 ** 20, 2 ** 25, dict(groups=65536, ldb=32, stride_b=0))):
+    for M, N, kw in ((2 ** 31 - 1, 2 ** 20, {}), (1, 2 ** 30, dict(a_type="bf16")), (2 ** 20, 2 ** 25, dict(groups=65536, ldb=32, stride_b=0))):
         with pytest.raises(dg.DgError) as e:
             dg.dg_gemm_scaled_describe(dg.make_scaled_desc(M, N, 32, **kw))
         assert e.value.status == NO
