@@ -264,7 +264,7 @@ __global__ __launch_bounds__(FEW_T) void dispatch_few_kernel(DispatchArgs a)
 
 // A wavefront takes 64 x U pieces of 16 bytes of one token's row and writes
 // them to each of its places: x is read once, whatever top_k is.
-constexpr int SPREAD_U = 4, SPREAD_T = 256;
+constexpr int SPREAD_U = 2, SPREAD_T = 256;
 
 __global__ __launch_bounds__(SPREAD_T) void spread_kernel(SpreadArgs a)
 {
