@@ -279,7 +279,6 @@ hipError_t launch_scaled_stream(int32_t variant, const ScaledArgs &a, uint32_t p
     case 2: return launch<1, 2, 4, 2>(a, programs, s);
     case 3: return launch<1, 4, 8, 1>(a, programs, s);
     case 4: return launch<2, 2, 8, 1>(a, programs, s);
-    case 5: return launch<2, 4, 8, 1>(a, programs, s);
     default: return hipErrorInvalidValue;
     }
 }

@@ -244,9 +244,10 @@ hipError_t launch_scaled_tile(int32_t variant, const ScaledArgs &a, uint32_t pro
     switch (variant) {
     case 0: return launch_any<64, 128>(a, programs, s);
     case 1: return launch_any<128, 128>(a, programs, s);
-    case 2: return launch<128, 128, 4>(a, programs, s);
-    case 3: return launch<128, 128, 2>(a, programs, s);
-    case 4: return launch_mixed(a, programs, s);
+    case 2: return launch<64, 128, 4>(a, programs, s);
+    case 3: return launch<128, 128, 4>(a, programs, s);
+    case 4: return launch<128, 128, 2>(a, programs, s);
+    case 5: return launch_mixed(a, programs, s);
     default: return hipErrorInvalidValue;
     }
 }

@@ -107,14 +107,14 @@ const ScaledKernel kS16x32 = {"i8_stream_16x32", 16, 32, 512, true, stream_kerne
 const ScaledKernel kS16x32short = {"i8_stream_16x32_short", 16, 32, 256, true, stream_kernel<2>, nullptr};
 const ScaledKernel kS16x64 = {"i8_stream_16x64", 16, 64, 512, true, stream_kernel<3>, few_kernel<2>};
 const ScaledKernel kS32x32 = {"i8_stream_32x32", 32, 32, 512, true, stream_kernel<4>, nullptr};
-const ScaledKernel kS32x64 = {"i8_stream_32x64", 32, 64, 512, true, stream_kernel<5>, nullptr};
 const ScaledKernel kAny64 = {"i8_any_64x128", 64, 128, 256, true, tile_kernel<0>, nullptr};
 const ScaledKernel kAny128 = {"i8_any_128x128", 128, 128, 256, true, tile_kernel<1>, nullptr};
-const ScaledKernel kT128deep = {"i8_tile_128x128_deep", 128, 128, 512, false, tile_kernel<2>, nullptr};
-const ScaledKernel kT128 = {"i8_tile_128x128", 128, 128, 512, false, tile_kernel<3>, nullptr};
-const ScaledKernel kT256 = {"i8_tile_256x256", 256, 256, 512, false, tile_kernel<4>, nullptr};
-const ScaledKernel *const kKernels[] = {&kS16x16, &kS16x32short, &kS16x32, &kS16x64, &kS32x32, &kS32x64,
-                                        &kAny64, &kAny128, &kT128deep, &kT128, &kT256};
+const ScaledKernel kT64 = {"i8_tile_64x128", 64, 128, 512, false, tile_kernel<2>, nullptr};
+const ScaledKernel kT128deep = {"i8_tile_128x128_deep", 128, 128, 512, false, tile_kernel<3>, nullptr};
+const ScaledKernel kT128 = {"i8_tile_128x128", 128, 128, 512, false, tile_kernel<4>, nullptr};
+const ScaledKernel kT256 = {"i8_tile_256x256", 256, 256, 512, false, tile_kernel<5>, nullptr};
+const ScaledKernel *const kKernels[] = {&kS16x16, &kS16x32short, &kS16x32, &kS16x64, &kS32x32,
+                                        &kAny64, &kT64, &kAny128, &kT128deep, &kT128, &kT256};
 
 struct ScaledPlan {
     const ScaledKernel *kernel;
@@ -156,16 +156,18 @@ double expected_tiles(const dg_scaled_desc *d, int64_t bm, int64_t bn)
 //     16);
 //   one matrix, up to 32 rows: 16 x 32 while that is one workgroup per
 //     compute unit (32 x 4096 x 4096 9.3 against 11.3 on 32 x 32);
-//   then 32-row ones while they are one workgroup per compute unit: 64 x 4096 x
-//     4096 11.4 on 32 x 32, 15.5 on 32 x 64, 17.7 on 128 x 128; 64 x 8192 x
-//     4096 18.8, 16.4, 19.0; 128 x 8192 x 4096 33.0, 28.9, 20.2; groups of 9
-//     to 16 rows 32 x 32 unless 128 x 128 tiles fill the chip twice (100 rows,
-//     8 groups, 4096 x 4096 33 against 36; 1024 rows, 64 groups, 2048 x 2048
-//     80 against 57.6, and 74 on 16 x 64);
-//   128 x 128 with a ring of four stages, one workgroup per compute unit, up
-//     to 256 tiles (1024 x 4096 x 4096 21.3 against 27.2 with two stages and
-//     30.3 on 256 x 256), with two stages and two workgroups above (2000 rows,
-//     16 groups, 4096 x 2048 46.9 against 48.9 and 51.4);
+//   then 32 x 32 while that is: 64 x 4096 x 4096 11.5 against 12.9 on 64 x 128;
+//     64 x 8192 x 4096 19.5 against 15.9; with groups up to 16 rows, unless
+//     128 x 128 tiles fill the chip twice (100 rows, 8 groups, 4096 x 4096 33
+//     against 36; 1024 rows, 64 groups, 2048 x 2048 80 against 57.6, and 74 on
+//     16 x 64);
+//   rings of four stages with one workgroup per compute unit up to 256 tiles,
+//     of 64 x 128 (256 x 4096 x 4096 13.5 against 17.6 on 128 x 128; 512 x 2048 x
+//     8192 21.3 and 29; 300 rows, 16 groups, 1024 x 2048 11.8 and 13.9; 1024 x
+//     4096 x 4096, 512 of them, 26.9 and 21.5), then of 128 x 128 (27.0 with two
+//     stages, 29.3 on 256 x 256);
+//   128 x 128 with two stages and two workgroups (2000 rows, 16 groups, 4096 x
+//     2048 46.2 against 47.4 with four and 51.7);
 //   256 x 256, cut in halves where that saves a wave, from half a chip of
 //     them, with groups of 256 rows from a whole chip (2048 x 4096 x 4096 35.1
 //     against 36.4 on 128 x 128; 4096 x 4096 x 4096 56 against 70; 8192 rows,
@@ -173,7 +175,7 @@ double expected_tiles(const dg_scaled_desc *d, int64_t bm, int64_t bn)
 //     4096, 144 of them, 61 against 59).
 // Off the 16-byte grid, or with odd K: the same streaming kernels, then tiles
 // filled through registers, 64 x 128 until 128 x 128 ones fill the chip twice
-// (64 x 4097 x 1001 14 against 17 on 32 x 64; 700 x 4097 x 1001 19 against 20
+// (64 x 4097 x 1001 14 against 17 on 32 x 64 streamed; 700 x 4097 x 1001 19 against 20
 // on 128 x 128, and 89; 2048 x 4096 x 4096 92 against 67).
 const ScaledKernel *choose(const dg_scaled_desc *d, bool tile)
 {
@@ -203,8 +205,8 @@ const ScaledKernel *choose(const dg_scaled_desc *d, bool tile)
         return &kS32x32;
     if (!tile)
         return t128 >= 512 ? &kAny128 : &kAny64;
-    if (!groups && expected_tiles(d, 32, 64) <= 256)
-        return &kS32x64;
+    if (expected_tiles(d, 64, 128) <= 256)
+        return &kT64;
     if (groups ? mean >= 256 && t256 >= 256 : t256 >= 128)
         return &kT256;
     return t128 <= 256 ? &kT128deep : &kT128;

@@ -14,8 +14,8 @@ from tokens_util import codes64, same_bits
 
 pytestmark = pytest.mark.gpu
 
-KERNELS = ["i8_stream_16x16", "i8_stream_16x32", "i8_stream_16x32_short", "i8_stream_16x64", "i8_stream_32x32", "i8_stream_32x64",
-           "i8_any_64x128", "i8_any_128x128", "i8_tile_128x128_deep", "i8_tile_128x128", "i8_tile_256x256"]
+KERNELS = ["i8_stream_16x16", "i8_stream_16x32", "i8_stream_16x32_short", "i8_stream_16x64", "i8_stream_32x32",
+           "i8_any_64x128", "i8_tile_64x128", "i8_any_128x128", "i8_tile_128x128_deep", "i8_tile_128x128", "i8_tile_256x256"]
 
 
 @pytest.fixture(scope="module", autouse=True)

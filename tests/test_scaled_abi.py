@@ -141,7 +141,8 @@ def _plan(text):
 @pytest.mark.parametrize("M,N,K,kw,kernel", [
     (1, 4096, 4096, {}, "i8_stream_16x16"), (16, 8192, 8192, {}, "i8_stream_16x32"),
     (13, 16384, 8192, {}, "i8_stream_16x64"), (64, 4096, 4096, {}, "i8_stream_32x32"),
-    (64, 8192, 4096, {}, "i8_stream_32x64"), (128, 8192, 4096, {}, "i8_tile_128x128_deep"),
+    (64, 8192, 4096, {}, "i8_tile_64x128"), (512, 4096, 4096, {}, "i8_tile_64x128"),
+    (300, 1024, 2048, dict(groups=16), "i8_tile_64x128"),
     (1024, 4096, 4096, {}, "i8_tile_128x128_deep"), (2048, 2560, 1024, {}, "i8_tile_128x128"),
     (2048, 4096, 4096, {}, "i8_tile_256x256"),
     (1, 4096, 4096, dict(a_type="bf16"), "i8_stream_16x16"), (1, 8192, 2048, dict(a_type="bf16"), "i8_stream_16x32"),
