@@ -117,24 +117,24 @@ __device__ __forceinline__ uint4 load_chunk(const int8_t *p)
 }
 
 template <int BM, int BN>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2)))
 void scaled_any_kernel(ScaledArgs a)
 {
     extern __shared__ uint4 lds[];
-    constexpr int ROWS = BM + BN, PER = ROWS / 32, TM = BM / 2, TN = BN / 2, FM = TM / 16, FN = TN / 16;
+    constexpr int ROWS = BM + BN, PER = ROWS / 64, TM = BM / 2, TN = BN / 4, FM = TM / 16, FN = TN / 16;
     const GroupTile t = scaled_tile<BM>(a);
     if (t.group < 0)
         return;
     const GemmArgs g = scaled_args(a, t.group, t.start, t.rows);
     const int64_t m0 = (int64_t)t.row_tile * BM, n0 = (int64_t)t.col_tile * BN;
     const int64_t last_row = (g.M - m0 < BM ? g.M - m0 : BM) - 1, last_col = (g.N - n0 < BN ? g.N - n0 : BN) - 1;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave / 2, wn = wave % 2;
-    // this thread's chunks: chunk tid % 8 of stage rows tid / 8 + 32 i
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave / 4, wn = wave % 4;
+    // this thread's chunks: chunk tid % 8 of stage rows tid / 8 + 64 i
     const int chunk = tid % 8;
     const int8_t *src[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int64_t r = tid / 8 + 32 * i;
+        const int64_t r = tid / 8 + 64 * i;
         src[i] = r < BM ? (const int8_t *)g.A + (m0 + (r < last_row ? r : last_row)) * g.lda
                         : (const int8_t *)g.B + (n0 + (r - BM < last_col ? r - BM : last_col)) * g.ldb;
         src[i] += 16 * chunk;
@@ -142,7 +142,7 @@ void scaled_any_kernel(ScaledArgs a)
     auto put = [&](int buffer, const uint4 (&from)[PER]) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int r = tid / 8 + 32 * i;
+            const int r = tid / 8 + 64 * i;
             lds[(buffer * ROWS + r) * 8 + (chunk ^ swizzle_key<8>(r))] = from[i];
         }
     };
@@ -217,7 +217,7 @@ void scaled_any_kernel(ScaledArgs a)
     }
     const TileCoord tc{0, 0, (int32_t)t.row_tile, (int32_t)t.col_tile};
     const RowColScales sc{row_scales(a, t.start), col_scales(a, t.group), a.scale_type};
-    scaled_epilogue<BM, BN, 2, 2, 256>(g, tc, (float *)lds, m0, n0, acc, sc);
+    scaled_epilogue<BM, BN, 2, 4, 256>(g, tc, (float *)lds, m0, n0, acc, sc);
 }
 
 template <int BM, int BN>
@@ -225,7 +225,7 @@ hipError_t launch_any(const ScaledArgs &a, uint32_t programs, hipStream_t s)
 {
     constexpr int stages = 2 * (BM + BN) * 128, lds = stages > scaled_epilogue_lds_bytes(BM, BN)
                                                           ? stages : scaled_epilogue_lds_bytes(BM, BN);
-    hipLaunchKernelGGL((scaled_any_kernel<BM, BN>), dim3(programs), dim3(256), (size_t)lds, s, a);
+    hipLaunchKernelGGL((scaled_any_kernel<BM, BN>), dim3(programs), dim3(512), (size_t)lds, s, a);
     return hipGetLastError();
 }
 

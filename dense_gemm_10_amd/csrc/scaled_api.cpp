@@ -107,8 +107,8 @@ const ScaledKernel kS16x32 = {"i8_stream_16x32", 16, 32, 512, true, stream_kerne
 const ScaledKernel kS16x32short = {"i8_stream_16x32_short", 16, 32, 256, true, stream_kernel<2>, nullptr};
 const ScaledKernel kS16x64 = {"i8_stream_16x64", 16, 64, 512, true, stream_kernel<3>, few_kernel<2>};
 const ScaledKernel kS32x32 = {"i8_stream_32x32", 32, 32, 512, true, stream_kernel<4>, nullptr};
-const ScaledKernel kAny64 = {"i8_any_64x128", 64, 128, 256, true, tile_kernel<0>, nullptr};
-const ScaledKernel kAny128 = {"i8_any_128x128", 128, 128, 256, true, tile_kernel<1>, nullptr};
+const ScaledKernel kAny64 = {"i8_any_64x128", 64, 128, 512, true, tile_kernel<0>, nullptr};
+const ScaledKernel kAny128 = {"i8_any_128x128", 128, 128, 512, true, tile_kernel<1>, nullptr};
 const ScaledKernel kT64 = {"i8_tile_64x128", 64, 128, 512, false, tile_kernel<2>, nullptr};
 const ScaledKernel kT128deep = {"i8_tile_128x128_deep", 128, 128, 512, false, tile_kernel<3>, nullptr};
 const ScaledKernel kT128 = {"i8_tile_128x128", 128, 128, 512, false, tile_kernel<4>, nullptr};
@@ -174,9 +174,10 @@ double expected_tiles(const dg_scaled_desc *d, int64_t bm, int64_t bn)
 //     16 groups, 4096 x 4096 168 against 195; but 8192 rows, 8 groups, 1024 x
 //     4096, 144 of them, 61 against 59).
 // Off the 16-byte grid, or with odd K: the same streaming kernels, then tiles
-// filled through registers, 64 x 128 until 128 x 128 ones fill the chip twice
-// (64 x 4097 x 1001 14 against 17 on 32 x 64 streamed; 700 x 4097 x 1001 19 against 20
-// on 128 x 128, and 89; 2048 x 4096 x 4096 92 against 67).
+// filled through registers, of 64 x 128 up to one per compute unit (64 x 4097 x
+// 1001 11.8 against 15.1 on 128 x 128, and 17 on 32 x 64 streamed; 300 x 4096 x
+// 4096 24.7 and 32.6), then of 128 x 128 (700 x 4097 x 1001 16.1 against 17.5;
+// 2048 x 4096 x 4096 61 against 88).
 const ScaledKernel *choose(const dg_scaled_desc *d, bool tile)
 {
     if (few_rows(d) && reads_ab(d)) {
@@ -200,12 +201,12 @@ const ScaledKernel *choose(const dg_scaled_desc *d, bool tile)
     }
     if (!groups && mean <= 32 && expected_tiles(d, 16, 32) <= 256)
         return d->K > 2048 ? &kS16x32 : &kS16x32short;
-    const double t128 = expected_tiles(d, 128, 128), t256 = expected_tiles(d, 256, 256);
+    const double t64 = expected_tiles(d, 64, 128), t128 = expected_tiles(d, 128, 128), t256 = expected_tiles(d, 256, 256);
     if (groups ? mean <= 16 && t128 <= 512 : expected_tiles(d, 32, 32) <= 256)
         return &kS32x32;
     if (!tile)
-        return t128 >= 512 ? &kAny128 : &kAny64;
-    if (expected_tiles(d, 64, 128) <= 256)
+        return t64 <= 256 ? &kAny64 : &kAny128;
+    if (t64 <= 256)
         return &kT64;
     if (groups ? mean >= 256 && t256 >= 256 : t256 >= 128)
         return &kT256;
