@@ -390,3 +390,59 @@ def test_layer_of_experts_and_its_gradients():
     for got, want, size in ((y, ref, big), (dx, x64.grad, xm.grad), (dW, W64.grad, Wm.grad), (dw, w64.grad, wm.grad)):
         err = (got.cpu().double() - want.detach()).abs()
         assert bool((err <= 3.1 * u * size.detach() + 1e-30).all())
+
+
+def test_many_tokens():
+    """More tokens than the launches have workgroups, slots in chunks of many rounds."""
+    tokens, width, groups = 4_400_000, 8, 40
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    index = torch.randint(-1, groups, (tokens, 1), device="cuda", generator=gen)
+    x = torch.randn(tokens, width, device="cuda", generator=gen).bfloat16()
+    rows, off, order, place = dg.dispatch_tokens(x, index, groups, out=torch.zeros_like(x))
+    key = torch.where(index[:, 0] < 0, groups, index[:, 0])
+    want = torch.sort(key, stable=True).indices
+    n = int((index >= 0).sum())
+    assert int(off[groups]) == n and torch.equal(order[:n].long(), want[:n]) and bool((order[n:] == -1).all())
+    assert torch.equal(off.long()[1:], torch.bincount(key, minlength=groups + 1)[:groups].cumsum(0))
+    assert torch.equal(rows[:n], x[want[:n]]) and bool((rows[n:] == 0).all())
+    kept = (index >= 0).expand_as(x)
+    assert torch.equal(dg.combine_tokens(rows, place), torch.where(kept, x, 0))
+    w = torch.full((tokens, 1), 2.0, device="cuda")
+    dz, dw = dg.combine_tokens_grad(x, rows, place, w, dz=torch.zeros_like(x))
+    assert torch.equal(dz, 2 * rows)
+    norm = torch.where(kept, x, 0).double().square().sum(1, keepdim=True)
+    assert bool(((dw.double() - norm).abs() <= 16 * 2.0 ** -23 * norm).all())
+    q, s = dg.quantize_rows(x, place, torch.zeros(tokens, width, dtype=torch.int8, device="cuda"),
+                            torch.zeros(tokens, device="cuda"))
+    top = rows.double().abs().amax(1, keepdim=True)
+    codes = torch.where(top > 0, 127 * rows.double() / top, 0.0).round()
+    assert torch.equal(q, codes.to(torch.int8)) and torch.equal(s, (top[:, 0] / 127).float())
+
+
+def test_two_streams_at_once():
+    gen = torch.Generator().manual_seed(13)
+    tokens, top_k, groups, width = 1500, 2, 16, 512
+    cases = []
+    for _ in range(2):
+        x = torch.randn(tokens, width, generator=gen).bfloat16().cuda()
+        index = random_index(tokens, top_k, groups, gen).cuda()
+        w = torch.rand(tokens, top_k, generator=gen).cuda()
+        B = torch.randint(-127, 128, (groups, 300, width), generator=gen, dtype=torch.int8).cuda()
+        cases.append((x, index, w, B))
+
+    def layer(x, index, w, B):
+        rows, off, _, place = dg.dispatch_tokens(x, index, groups)
+        return dg.combine_tokens(dg.gemm_scaled(rows, B, offsets=off), place, w), dg.combine_tokens(rows, place)
+
+    want = [layer(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(10):
+        for i, (stream, c) in enumerate(zip(streams, cases)):
+            with torch.cuda.stream(stream):
+                got[i].append(layer(*c))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        for out in g:
+            assert all(same_bits(a, b) for a, b in zip(out, w))
