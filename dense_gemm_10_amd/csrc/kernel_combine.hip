@@ -1,6 +1,13 @@
 // Rows brought back to their tokens, and the gradients.  Memory bound: every
 // row of z is read once, every output written once, no LDS in the forward
-// pass.
+// pass.  A sum is one chain of fused multiply-adds in the order of j, a dot
+// product one per lane and column of eight, added over the lanes in a fixed
+// order: calls repeat bit for bit.
+//
+// Measured (MI355X, 8192 tokens, 2 rows each, 4096 bf16, kernel times, operands
+// the same from call to call): forward 32 us, 202 MB moved, 6.3 TB/s; gradients
+// 51 us, 337 MB, 6.6 TB/s.  With new operands in every call the two together
+// take 101 us, 5.3 TB/s.
 #include "grouped.hpp"
 #include "tokens.hpp"
 

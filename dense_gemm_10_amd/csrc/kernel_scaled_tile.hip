@@ -1,6 +1,13 @@
 // 8-bit products on the tiles of mfma16.hpp: rows on 16 bytes, K a whole
 // number of pairs.  Everything up to the MFMA sees 16-bit elements, two
 // integers each.
+//
+// Measured (MI355X, bf16 out, codes uniform in +-127): 16384^3 2.68 POP/s, 8192^3
+// 2.77, 4096^3 2.14 (64 us).  Fitted over K, a 256 x 256 tile takes 1.5 us a
+// stage of 128 bytes and 12 us beside its stages (16 with the tanh GELU, 19.5
+// with the erf form).  The matrix pipe is busy 64 % of the cycles at 2.0 GHz,
+// without bank conflicts; 61 % in the 16-bit kernel of the same bytes.  8192
+// rows, 16 groups, 4096 x 4096 with bias and erf GELU 178 to 195 us.
 #include "grouped16.hpp"
 #include "scaled.hpp"
 
@@ -24,7 +31,8 @@ __device__ __forceinline__ GemmArgs in_pairs(GemmArgs g)
 // 256 that vector instructions read.  With four wavefronts and sums in both
 // halves of the register file the compiler copies them back and forth in the
 // K loop, and without the copies one wavefront per SIMD is slower still
-// (4096 x 4096 x 4096: 62 us against 54; with the copies 80).
+// (4096 x 4096 x 4096: 62 us against 54; 8192 rows, 16 groups,
+// 4096 x 4096 with the copies 260 us a call, 203 with them suppressed).
 template <int BM, int BN, int NS>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2)))
 void scaled_tile_kernel(ScaledArgs a)
