@@ -11,6 +11,7 @@ import sys
 
 from . import DG_F32, DG_SUCCESS, DgError, _ACT, _DTYPE, _enum, _load
 from .grouped import _bias, _check_offsets, _code, _launch, _output, _row_ld, _same_device
+from .tokens import _there
 
 DG_I8 = 3
 DG_SCALED_FEW_ROWS, DG_SCALED_FEW_ELEMENTS = 4, 8192
@@ -110,7 +111,11 @@ def gemm_scaled(A, B, scale_a=None, scale_b=None, C=None, *, offsets=None, alpha
     leading dimension of groups, and each row of A uses its group's; rows of no
     group are left alone.  out_dtype defaults to a float A's type, else bf16.
     Rows of A and B that start on 16 bytes and even K run fastest (quantize_rows
-    allocates them so, of weights too)."""
+    allocates them so, of weights too).  With stream (a hipStream_t as int) the
+    call runs there, and C and the workspace are allocated there."""
+    if stream is not None:
+        return _there(stream, A, gemm_scaled, A, B, scale_a, scale_b, C, offsets=offsets, alpha=alpha, beta=beta,
+                      bias=bias, act=act, out_dtype=out_dtype)
     torch = sys.modules["torch"]
     int8 = torch.int8
     ashape, bshape = A.shape, B.shape
@@ -151,8 +156,6 @@ def gemm_scaled(A, B, scale_a=None, scale_b=None, C=None, *, offsets=None, alpha
     desc = _pack(_SIZE, _code(A) if own else DG_I8, _code(C), sb_type, bias_type, _enum(_ACT, act), groups, M, N, K,
                  _row_ld(M, K, *A.stride(), "A"), _row_ld(N, K, *bstride[-2:], "B"),
                  _row_ld(M, N, *C.stride(), "C"), stride_b, stride_s, stride_bias, alpha, beta, bias_ptr)
-    _launch(_fast(), "dg_gemm_scaled", device, stream, desc, A.data_ptr(), sa, B.data_ptr(), sb, C.data_ptr(),
+    _launch(_fast(), "dg_gemm_scaled", device, None, desc, A.data_ptr(), sa, B.data_ptr(), sb, C.data_ptr(),
             offsets.data_ptr() if grouped else None, None if ws is None else ws.data_ptr(), ws_bytes)
-    if ws is not None and stream is not None:
-        ws.record_stream(torch.cuda.ExternalStream(stream, A.device))     # not reused before the call is done there
     return C

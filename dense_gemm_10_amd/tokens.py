@@ -5,7 +5,8 @@ dg_dispatch, dg_spread, dg_combine, dg_combine_grad and dg_quantize
 Argument marshalling only, like the rest of the package: checks of shapes,
 types, strides and devices, one descriptor, one call on the current stream.
 Nothing is copied or cast, and nothing allocated but the results that are not
-given.
+given.  With ``stream`` (a hipStream_t as int) the call runs there, and what it
+allocates belongs to that stream.
 """
 from __future__ import annotations
 
@@ -139,6 +140,15 @@ def _torch():
     return sys.modules["torch"]           # a tensor was passed: it is imported
 
 
+def _there(stream, like, call, *args, **named):
+    """call(...) with `stream` current: new tensors come from its own memory,
+    which no other stream's pending work can still be using."""
+    torch = _torch()
+    _same_device(like.get_device())
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, like.device)):
+        return call(*args, **named)
+
+
 def _ld(t, rows, cols, name):
     """Leading dimension of a row-major 2-D tensor."""
     return cols or 1 if t.is_contiguous() else _row_ld(rows, cols, *t.stride(), name)
@@ -194,11 +204,13 @@ def _maps(index, groups):
 
 def sort_tokens(index, groups, *, stream=None):
     """The maps of dispatch_tokens alone: (offsets, order, place)."""
+    if stream is not None:
+        return _there(stream, index, sort_tokens, index, groups)
     tokens, top_k, ld, bits, offsets, order, place = _maps(index, groups)
     device = index.get_device()
     _same_device(device)
     desc = _pack_dispatch(_DISPATCH_SIZE, DG_F32, bits, tokens, top_k, groups, 0, 0, ld, 1, 1)
-    _launch(_fast("dg_dispatch"), "dg_dispatch", device, stream, desc, index.data_ptr(), None,
+    _launch(_fast("dg_dispatch"), "dg_dispatch", device, None, desc, index.data_ptr(), None,
             offsets.data_ptr(), order.data_ptr(), place.data_ptr(), None)
     return offsets, order, place
 
@@ -214,6 +226,8 @@ def dispatch_tokens(x, index, groups, *, out=None, stream=None):
     every slot, -1 for none.  Slots of one group keep their order.  Rows from
     offsets[groups] on keep what ``out`` held (in rows allocated here: nothing
     defined) and have order -1."""
+    if stream is not None:
+        return _there(stream, x, dispatch_tokens, x, index, groups, out=out)
     n, width, ldx = _matrix(x, "x")
     tokens, top_k, ld, bits, offsets, order, place = _maps(index, groups)
     if n != tokens:
@@ -223,7 +237,7 @@ def dispatch_tokens(x, index, groups, *, out=None, stream=None):
     _on_device(device, index=index, out=rows)
     desc = _pack_dispatch(_DISPATCH_SIZE, _code(x), bits, tokens, top_k, groups, tokens * top_k, width, ld, ldx,
                           _ld(rows, tokens * top_k, width, "out"))
-    _launch(_fast("dg_dispatch"), "dg_dispatch", device, stream, desc, index.data_ptr(), x.data_ptr(),
+    _launch(_fast("dg_dispatch"), "dg_dispatch", device, None, desc, index.data_ptr(), x.data_ptr(),
             offsets.data_ptr(), order.data_ptr(), place.data_ptr(), rows.data_ptr())
     return rows, offsets, order, place
 
@@ -233,6 +247,8 @@ def spread_tokens(x, place, *, out=None, stream=None):
     dispatch_tokens from its place, and the gradient of combine_tokens without
     weights.  ``out`` may have any number of rows; a place outside them is
     skipped.  Returns rows (tokens * top_k, width by default)."""
+    if stream is not None:
+        return _there(stream, x, spread_tokens, x, place, out=out)
     n, width, ldx = _matrix(x, "x")
     tokens, top_k = _check_place(place)
     if n != tokens:
@@ -242,7 +258,7 @@ def spread_tokens(x, place, *, out=None, stream=None):
     _on_device(device, place=place, out=rows)
     desc = _pack_dispatch(_DISPATCH_SIZE, _code(x), 32, tokens, top_k, 0, rows.shape[0], width, max(1, top_k), ldx,
                           _ld(rows, rows.shape[0], width, "out"))
-    _launch(_fast("dg_spread"), "dg_spread", device, stream, desc, place.data_ptr(), x.data_ptr(),
+    _launch(_fast("dg_spread"), "dg_spread", device, None, desc, place.data_ptr(), x.data_ptr(),
             rows.data_ptr())
     return rows
 
@@ -264,6 +280,8 @@ def combine_tokens(z, place, weights=None, y=None, *, beta=0.0, out_dtype=None, 
     dispatch_tokens.  weights: (tokens, top_k) of any float type, or None for
     ones (the gradient of dispatch_tokens and spread_tokens).  y: z's type or
     fp32.  Returns y (tokens, width)."""
+    if stream is not None:
+        return _there(stream, z, combine_tokens, z, place, weights, y, beta=beta, out_dtype=out_dtype)
     rows, width, ldz = _matrix(z, "z")
     tokens, top_k = _check_place(place)
     if y is None and beta != 0.0:
@@ -274,7 +292,7 @@ def combine_tokens(z, place, weights=None, y=None, *, beta=0.0, out_dtype=None, 
     w, wt, ldw = _weights(weights, (tokens, top_k))
     desc = _pack_combine(_COMBINE_SIZE, _code(z), _code(y), wt, tokens, top_k, rows, width, ldz, ldz,
                          _ld(y, tokens, width, "y"), ldw, beta)
-    _launch(_fast("dg_combine"), "dg_combine", device, stream, desc, z.data_ptr(), place.data_ptr(), w,
+    _launch(_fast("dg_combine"), "dg_combine", device, None, desc, z.data_ptr(), place.data_ptr(), w,
             y.data_ptr())
     return y
 
@@ -285,6 +303,8 @@ def combine_tokens_grad(dy, z, place, weights, *, dz=None, stream=None):
     z[place[t, j]]>, 0 for a slot without a row.  dy: (tokens, width), z's type
     or fp32; dweights has weights' type.  Rows that no slot has keep what
     ``dz`` held (in a dz allocated here: nothing defined)."""
+    if stream is not None:
+        return _there(stream, z, combine_tokens_grad, dy, z, place, weights, dz=dz)
     n, width, ldy = _matrix(dy, "dy")
     rows, zw, ldz = _matrix(z, "z")
     tokens, top_k = _check_place(place)
@@ -299,7 +319,7 @@ def combine_tokens_grad(dy, z, place, weights, *, dz=None, stream=None):
     _on_device(device, dy=dy, place=place, weights=weights, dz=dz)
     desc = _pack_combine(_COMBINE_SIZE, _code(z), _code(dy), wt, tokens, top_k, rows, width, ldz,
                          _ld(dz, rows, width, "dz"), ldy, ldw, 0.0)
-    _launch(_fast("dg_combine_grad"), "dg_combine_grad", device, stream, desc, dy.data_ptr(), z.data_ptr(),
+    _launch(_fast("dg_combine_grad"), "dg_combine_grad", device, None, desc, dy.data_ptr(), z.data_ptr(),
             place.data_ptr(), w, dz.data_ptr(), dw.data_ptr())
     return dz, dw
 
@@ -314,6 +334,8 @@ def quantize_rows(x, place=None, q=None, scales=None, *, stream=None):
     t's codes and scale go to the rows place[t, j].  Returns (q, scales): int8
     (rows, width), each row starting on 16 bytes if allocated here, and fp32
     (rows,)."""
+    if stream is not None:
+        return _there(stream, x, quantize_rows, x, place, q, scales)
     torch = _torch()
     tokens, width, ldx = _matrix(x, "x")
     top_k = 1
@@ -332,6 +354,6 @@ def quantize_rows(x, place=None, q=None, scales=None, *, stream=None):
     _on_device(device, place=place, q=q, scales=scales)
     desc = _pack_quantize(_QUANTIZE_SIZE, _code(x), tokens, top_k, rows, width, ldx,
                           _ld(q, rows, width, "q"))
-    _launch(_fast("dg_quantize"), "dg_quantize", device, stream, desc, x.data_ptr(),
+    _launch(_fast("dg_quantize"), "dg_quantize", device, None, desc, x.data_ptr(),
             None if place is None else place.data_ptr(), q.data_ptr(), scales.data_ptr())
     return q, scales

@@ -501,7 +501,8 @@ dg_status dg_combine_grad(const dg_combine_desc *d, const void *dy, const void *
  * a row that holds an infinity or NaN gets scale NaN and codes 0.  With
  * `place` (tokens x top_k int32, packed, as dg_dispatch writes it) the codes
  * and scale of token t go to the rows place[t][j] of q and scales, in
- * [0, rows); other rows are left as they were.  place NULL: row t, and rows
+ * [0, rows); other rows are left as they were, and a row that two tokens have
+ * gets codes of either.  place NULL: row t, and rows
  * and top_k are ignored.
  *   x_type any dg_dtype; ldx, ldq >= max(1, width); tokens * top_k and rows
  *   at most 2^31 - 1. */

@@ -322,3 +322,42 @@ def test_8_bit_layer_of_experts_captured():
             for a, b in zip(out, layer()):
                 assert same_bits(a, b)
         torch.cuda.synchronize()
+
+
+def test_explicit_stream_leaves_the_current_streams_memory_alone():
+    """With stream=, what the call allocates must not be a block that the
+    current stream freed while work on it is still pending there."""
+    M, N, K = 512, 256, 4096
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    x = torch.randn(M, K, device="cuda", generator=gen).bfloat16()
+    B = torch.randint(-127, 128, (N, K), device="cuda", generator=gen, dtype=torch.int8)
+    sb = torch.rand(N, device="cuda", generator=gen)
+    at = torch.randint(0, 8, (M, 2), device="cuda", generator=gen)
+    want = dg.gemm_scaled(x, B, None, sb)
+    ones = torch.ones(M, 2, device="cuda")
+    side = torch.cuda.Stream()
+    sizes = (M * (K + 4), M * N * 2, 2 * M * K * 2, 2 * M * 4, M * K)     # workspace, C, rows, maps, codes
+    torch.cuda.synchronize()
+    freed = [torch.full((n,), 85, dtype=torch.uint8, device="cuda") for n in sizes]
+    spans = [(f.data_ptr(), f.data_ptr() + n) for f, n in zip(freed, sizes)]
+    kept = [torch.empty_like(f) for f in freed]
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda._sleep(20_000_000)
+    for k, f in zip(kept, freed):
+        k.copy_(f)
+    freed = f = None
+    got = dg.gemm_scaled(x, B, None, sb, stream=side.cuda_stream)
+    rows, offsets, order, place = dg.dispatch_tokens(x, at, 8, stream=side.cuda_stream)
+    q, s = dg.quantize_rows(x, stream=side.cuda_stream)
+    y = dg.combine_tokens(rows, place, stream=side.cuda_stream)
+    dz, dw = dg.combine_tokens_grad(x, rows, place, ones, stream=side.cuda_stream)
+    maps = dg.sort_tokens(at, 8, stream=side.cuda_stream)
+    spread = dg.spread_tokens(x, place, stream=side.cuda_stream)
+    torch.cuda.synchronize()
+    for t in (got, rows, offsets, order, place, q, s, y, dz, dw, *maps, spread):
+        assert not any(lo <= t.data_ptr() < hi for lo, hi in spans)
+    for k in kept:
+        assert bool((k == 85).all())
+    assert torch.equal(got, want)
+    assert torch.equal(spread, rows)
+    assert all(torch.equal(a, b) for a, b in zip(maps, (offsets, order, place)))
