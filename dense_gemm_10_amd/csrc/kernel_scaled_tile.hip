@@ -3,7 +3,7 @@
 // integers each.
 //
 // Measured (MI355X, bf16 out, codes uniform in +-127): 16384^3 2.68 POP/s, 8192^3
-// 2.77, 4096^3 2.14 (64 us).  Fitted over K, a 256 x 256 tile takes 1.5 us a
+// 2.77, 4096^3 2.42 (57 us; 63 to 66 in the first calls).  Fitted over K, a 256 x 256 tile takes 1.5 us a
 // stage of 128 bytes and 12 us beside its stages (16 with the tanh GELU, 19.5
 // with the erf form).  The matrix pipe is busy 64 % of the cycles at 2.0 GHz,
 // without bank conflicts; 61 % in the 16-bit kernel of the same bytes.  8192
