@@ -144,8 +144,11 @@ def _there(stream, like, call, *args, **named):
     """call(...) with `stream` current: new tensors come from its own memory,
     which no other stream's pending work can still be using."""
     torch = _torch()
-    _same_device(like.get_device())
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, like.device)):
+    device = like.get_device()
+    _same_device(device)
+    # ExternalStream(0) is a stream of torch's pool, not the null stream
+    there = torch.cuda.ExternalStream(stream, like.device) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(there):
         return call(*args, **named)
 
 
