@@ -268,6 +268,8 @@ dg_status dg_combine_grad(const dg_combine_desc *d, const void *dy, const void *
     a.dz = (char *)dz;
     a.dw = dweights;
     a.lddz = d->lddz * ez;
+    if (!reads)
+        a.width = 0;                       // dweights = 0; dy and z may be null
     return launch_combine_grad(a, (hipStream_t)stream) == hipSuccess ? DG_SUCCESS : DG_ERROR_LAUNCH;
 }
 

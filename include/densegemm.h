@@ -484,8 +484,9 @@ dg_status dg_spread(const dg_dispatch_desc *d, const int32_t *place, const void 
 dg_status dg_combine(const dg_combine_desc *d, const void *z, const int32_t *place,
                      const void *weights, void *y, void *stream);
 
-/* dz or dweights may be NULL (not wanted); z is read for dweights only.  beta
- * is ignored.  weights NULL: ones. */
+/* dz or dweights may be NULL (not wanted); z is read for dweights only, and
+ * neither dy nor z where rows or width is 0.  beta is ignored.  weights NULL:
+ * ones. */
 dg_status dg_combine_grad(const dg_combine_desc *d, const void *dy, const void *z,
                           const int32_t *place, const void *weights, void *dz, void *dweights,
                           void *stream);
