@@ -13,6 +13,7 @@ missing, loading raises instead of falling back to anything else.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -249,8 +250,13 @@ def gemm(A, B, C=None, *, alpha=1.0, beta=0.0, bias=None, act="none", out_dtype=
     """C = act(alpha * A @ B + beta * C + bias) on the current HIP stream.
 
     A: (M, K) or (batch, M, K); B: (K, N) or (batch, K, N); a batch
-    stride of 0 (``expand``) broadcasts.  Returns C (allocated when None)."""
+    stride of 0 (``expand``) broadcasts.  Returns C (allocated when None).
+    With stream (a hipStream_t as int) the call runs there, and what it
+    allocates belongs to that stream."""
     import torch
+    if stream is not None and C is None:
+        return _there(stream, A, gemm, A, B, alpha=alpha, beta=beta, bias=bias, act=act, out_dtype=out_dtype,
+                      split_k=split_k, group_m=group_m, algo=algo, xcd_remap=xcd_remap, workspace=workspace)
     batched = A.dim() == 3 or B.dim() == 3
     batch = A.shape[0] if A.dim() == 3 else (B.shape[0] if B.dim() == 3 else 1)
     M, K = A.shape[-2], A.shape[-1]
@@ -278,21 +284,23 @@ def gemm(A, B, C=None, *, alpha=1.0, beta=0.0, bias=None, act="none", out_dtype=
                      bias=bias.data_ptr() if bias is not None else None,
                      bias_type=_torch_dtype_name(bias) if bias is not None else "f32",
                      act=act, split_k=split_k, group_m=group_m, algo=algo, xcd_remap=xcd_remap)
-    if stream is None:
-        stream = torch.cuda.current_stream(A.device).cuda_stream
     ws_ptr, ws_bytes = None, 0
     if split_k != 1:
         need = dg_gemm_workspace_size(desc)
         if need:
             if workspace is None:
-                workspace = torch.empty(need, dtype=torch.uint8, device=A.device)
+                there = contextlib.nullcontext() if stream is None else torch.cuda.stream(_stream_of(stream, A))
+                with there:
+                    workspace = torch.empty(need, dtype=torch.uint8, device=A.device)
             ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if stream is None:
+        stream = torch.cuda.current_stream(A.device).cuda_stream
     dg_gemm(desc, A.data_ptr(), B.data_ptr(), C.data_ptr(), ws_ptr, ws_bytes, stream)
     return C
 
 
 from .grouped import (  # noqa: E402  (uses the names above)
-    DG_RAGGED_K, DG_RAGGED_M, DgGroupedDesc, DgQweightDesc, dg_gemm_grouped,
+    DG_RAGGED_K, DG_RAGGED_M, DgGroupedDesc, DgQweightDesc, _stream_of, _there, dg_gemm_grouped,
     dg_gemm_grouped_describe, dg_gemm_qweight, dg_gemm_qweight_describe, gemm_grouped,
     gemm_grouped_k, gemm_qweight, make_grouped_desc, make_qweight_desc)
 from .tokens import (  # noqa: E402

@@ -3,7 +3,9 @@ of dg_gemm_grouped and dg_gemm_qweight (include/densegemm.h).
 
 Argument marshalling only, like the rest of the package: checks of shapes,
 types, strides and devices, one descriptor, one call on the current stream.
-Nothing is copied, cast or allocated, apart from C when none is given.
+Nothing is copied, cast or allocated, apart from C when none is given.  With
+``stream`` (a hipStream_t as int) the call runs there, and such a C belongs to
+that stream.
 """
 from __future__ import annotations
 
@@ -220,6 +222,22 @@ def _launch(entry, name, device, stream, *args):
         raise DgError(st, name)
 
 
+def _stream_of(stream, like):
+    """The torch stream of a hipStream_t (int) on `like`'s device."""
+    torch = sys.modules["torch"]
+    device = like.get_device()
+    _same_device(device)
+    # ExternalStream(0) is a stream of torch's pool, not the null stream
+    return torch.cuda.ExternalStream(stream, like.device) if stream else torch.cuda.default_stream(device)
+
+
+def _there(stream, like, call, *args, **named):
+    """call(...) with `stream` current: new tensors come from its own memory,
+    which no other stream's pending work can still be using."""
+    with sys.modules["torch"].cuda.stream(_stream_of(stream, like)):
+        return call(*args, **named)
+
+
 def gemm_grouped(A, B, offsets, C=None, *, alpha=1.0, beta=0.0, bias=None, act="none",
                  out_dtype=None, stream=None):
     """C[i] = act(alpha * A[i] @ B[e] + beta * C[i] + bias[e]) for the rows i
@@ -230,6 +248,9 @@ def gemm_grouped(A, B, offsets, C=None, *, alpha=1.0, beta=0.0, bias=None, act="
     offsets: int32 (groups + 1,) on the GPU.  bias: (groups, N) or (N,).
     Returns C (rows, N); rows of no group keep what they held (in a C
     allocated here: nothing defined)."""
+    if stream is not None and C is None:
+        return _there(stream, A, gemm_grouped, A, B, offsets, alpha=alpha, beta=beta, bias=bias, act=act,
+                      out_dtype=out_dtype)
     ashape, bshape = A.shape, B.shape
     if len(ashape) != 2 or len(bshape) != 3 or ashape[1] != bshape[1]:
         raise ValueError(f"A {tuple(ashape)} and B {tuple(bshape)}: (rows, K) and (groups, K, N) are wanted")
@@ -263,6 +284,8 @@ def gemm_grouped_k(A, B, offsets, C=None, *, alpha=1.0, beta=0.0, out_dtype=None
     A: (M, rows), column-major (X is (rows, M) row-major).  B: (rows, N),
     row-major.  offsets as in gemm_grouped.  Returns C (groups, M, N); an
     empty group's is beta * C[e], or zeros."""
+    if stream is not None and C is None:
+        return _there(stream, A, gemm_grouped_k, A, B, offsets, alpha=alpha, beta=beta, out_dtype=out_dtype)
     ashape, bshape = A.shape, B.shape
     if len(ashape) != 2 or len(bshape) != 2 or ashape[1] != bshape[0]:
         raise ValueError(f"A {tuple(ashape)} and B {tuple(bshape)}: (M, rows) and (rows, N) are wanted")
@@ -295,6 +318,9 @@ def gemm_qweight(A, Q, scales, zeros=None, C=None, *, group_size, offsets=None, 
     None for 8.  With offsets (int32, groups + 1, on the GPU), Q, scales,
     zeros and optionally bias have a leading dimension of groups, and each
     row of A uses its group's weights; rows of no group are left alone."""
+    if stream is not None and C is None:
+        return _there(stream, A, gemm_qweight, A, Q, scales, zeros, group_size=group_size, offsets=offsets,
+                      alpha=alpha, beta=beta, bias=bias, act=act, out_dtype=out_dtype)
     uint8 = sys.modules["torch"].uint8
     ashape, qshape, sshape = A.shape, Q.shape, scales.shape
     grouped = offsets is not None

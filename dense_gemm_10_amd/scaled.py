@@ -10,8 +10,7 @@ import struct
 import sys
 
 from . import DG_F32, DG_SUCCESS, DgError, _ACT, _DTYPE, _enum, _load
-from .grouped import _bias, _check_offsets, _code, _launch, _output, _row_ld, _same_device
-from .tokens import _there
+from .grouped import _bias, _check_offsets, _code, _launch, _output, _row_ld, _same_device, _there
 
 DG_I8 = 3
 DG_SCALED_FEW_ROWS, DG_SCALED_FEW_ELEMENTS = 4, 8192

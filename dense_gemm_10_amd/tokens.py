@@ -15,7 +15,7 @@ import struct
 import sys
 
 from . import DG_F32, DG_SUCCESS, DgError, _DTYPE, _enum, _load
-from .grouped import _code, _launch, _row_ld, _same_device
+from .grouped import _code, _launch, _row_ld, _same_device, _there
 
 _i32, _i64, _f32, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
 
@@ -138,18 +138,6 @@ def dg_quantize(desc, x, place, q, scales, stream=None, check=True):
 # ---- torch convenience -----------------------------------------------------------
 def _torch():
     return sys.modules["torch"]           # a tensor was passed: it is imported
-
-
-def _there(stream, like, call, *args, **named):
-    """call(...) with `stream` current: new tensors come from its own memory,
-    which no other stream's pending work can still be using."""
-    torch = _torch()
-    device = like.get_device()
-    _same_device(device)
-    # ExternalStream(0) is a stream of torch's pool, not the null stream
-    there = torch.cuda.ExternalStream(stream, like.device) if stream else torch.cuda.default_stream(device)
-    with torch.cuda.stream(there):
-        return call(*args, **named)
 
 
 def _ld(t, rows, cols, name):
