@@ -271,8 +271,8 @@ dg_status dg_gemm_scaled(const dg_scaled_desc *d, const void *A, const float *sc
     if (make && (!workspace || workspace_bytes < (size_t)sp.workspace))
         return DG_ERROR_INSUFFICIENT_WORKSPACE;
     const struct { const void *p; int64_t n; } others[] = {
-        {A, reads ? sp.a : 0}, {B, reads ? sp.b : 0}, {scale_a, reads ? sp.sa : 0}, {scale_b, reads ? sp.sb : 0},
-        {d->bias, sp.bias}, {offsets, sp.offsets}};
+        {A, reads ? sp.a : 0}, {B, reads ? sp.b : 0}, {scale_a, d->alpha != 0.0f ? sp.sa : 0},
+        {scale_b, d->alpha != 0.0f ? sp.sb : 0}, {d->bias, sp.bias}, {offsets, sp.offsets}};
     for (const auto &o : others)
         if (ranges_overlap(C, sp.c, o.p, o.n) || (make && ranges_overlap(workspace, sp.workspace, o.p, o.n)))
             return DG_ERROR_INVALID_VALUE;

@@ -180,3 +180,10 @@ def test_launches_past_the_limit_are_refused():
         with pytest.raises(dg.DgError) as e:
             dg.dg_gemm_scaled_describe(dg.make_scaled_desc(M, N, 32, **kw))
         assert e.value.status == NO
+
+
+def test_scales_that_are_read_may_not_lie_in_c():
+    """They are read wherever alpha is not 0, without any K too."""
+    for K in (0, 64):
+        for kw in (dict(C=PSA), dict(C=PSB - 8)):
+            assert _run(_d(K=K), **kw) == BAD, (K, kw)
