@@ -6,7 +6,8 @@ the ABI's names (dg_gemm, dg_gemm_workspace_size, dg_gemm_describe,
 dg_status_string, dg_version, dg_schedule_map, dg_gemm_noalloc).  ``gemm()`` is a
 convenience wrapper for torch tensors; torch is used for device memory and
 streams only.  The products over groups of rows and with 4-bit weights are
-bound in grouped.py and named here too.
+bound in grouped.py, routed tokens and 8-bit codes in tokens.py, the products
+in 8-bit integers in scaled.py, and all of them named here too.
 
 The shared library is built in-tree by ``dense_gemm_10_amd.build``; if it is
 missing, loading raises instead of falling back to anything else.
@@ -28,6 +29,11 @@ __all__ = [
     "DG_RAGGED_M", "DG_RAGGED_K", "DgGroupedDesc", "DgQweightDesc", "make_grouped_desc",
     "make_qweight_desc", "dg_gemm_grouped", "dg_gemm_grouped_describe", "dg_gemm_qweight",
     "dg_gemm_qweight_describe", "gemm_grouped", "gemm_grouped_k", "gemm_qweight",
+    "DgDispatchDesc", "DgCombineDesc", "DgQuantizeDesc", "make_dispatch_desc", "make_combine_desc",
+    "make_quantize_desc", "dg_dispatch", "dg_spread", "dg_combine", "dg_combine_grad", "dg_quantize",
+    "sort_tokens", "dispatch_tokens", "spread_tokens", "combine_tokens", "combine_tokens_grad", "quantize_rows",
+    "DG_I8", "DG_SCALED_FEW_ROWS", "DG_SCALED_FEW_ELEMENTS", "DgScaledDesc", "make_scaled_desc", "dg_gemm_scaled",
+    "dg_gemm_scaled_workspace_size", "dg_gemm_scaled_describe", "gemm_scaled",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -308,5 +314,5 @@ from .tokens import (  # noqa: E402
     dg_combine_grad, dg_dispatch, dg_quantize, dg_spread, dispatch_tokens, make_combine_desc,
     make_dispatch_desc, make_quantize_desc, quantize_rows, sort_tokens, spread_tokens)
 from .scaled import (  # noqa: E402
-    DG_I8, DgScaledDesc, dg_gemm_scaled, dg_gemm_scaled_describe, dg_gemm_scaled_workspace_size, gemm_scaled,
-    make_scaled_desc)
+    DG_I8, DG_SCALED_FEW_ELEMENTS, DG_SCALED_FEW_ROWS, DgScaledDesc, dg_gemm_scaled, dg_gemm_scaled_describe,
+    dg_gemm_scaled_workspace_size, gemm_scaled, make_scaled_desc)
