@@ -149,7 +149,7 @@ void grouped_m_mixed_kernel(GroupedArgs a)
     const TileCoord tc{0, 0, (int32_t)t.row_tile, (int32_t)t.col_tile};
     if (!t.half)
         mfma16_tile<T, 256, 256, 2, 2, 2, 64, false, BT, 16>(g, tc, 0, g.K, nullptr, lds);
-    else if (tc.pid_m * 128 < t.rows)             // a cut tile's lower half may be empty
+    else                                          // never empty: a whole tile has more than 128 rows
         mfma16_tile<T, 128, 256, 2, 2, 3, 64, false, BT, 16>(g, tc, 0, g.K, nullptr, lds);
 }
 

@@ -104,7 +104,7 @@ void scaled_mixed_kernel(ScaledArgs a)
     const RowColScales sc{row_scales(a, t.start), col_scales(a, t.group), a.scale_type};
     if (!t.half)
         mfma16_tile<DT_I8, 256, 256, 2, 4, 2, 64, false, false, 16>(g, tc, 0, g.K, nullptr, lds, sc);
-    else if (tc.pid_m * 128 < t.rows)             // a cut tile's lower half may be empty
+    else                                          // never empty: a whole tile has more than 128 rows
         mfma16_tile<DT_I8, 128, 256, 2, 4, 3, 64, false, false, 16>(g, tc, 0, g.K, nullptr, lds, sc);
 }
 
