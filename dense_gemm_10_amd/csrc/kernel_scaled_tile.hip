@@ -3,11 +3,13 @@
 // integers each.
 //
 // Measured (MI355X, bf16 out, codes uniform in +-127): 16384^3 2.68 POP/s, 8192^3
-// 2.77, 4096^3 2.42 (57 us; 63 to 66 in the first calls).  Fitted over K, a 256 x 256 tile takes 1.5 us a
-// stage of 128 bytes and 12 us beside its stages (16 with the tanh GELU, 19.5
-// with the erf form).  The matrix pipe is busy 64 % of the cycles at 2.0 GHz,
-// without bank conflicts; 61 % in the 16-bit kernel of the same bytes.  8192
-// rows, 16 groups, 4096 x 4096 with bias and erf GELU 178 to 195 us.
+// 2.77, 4096^3 2.42 (57 us in the steady state; 63 to 66 in the first calls).
+// Fitted over K in the steady state, a whole 256 x 256 tile takes 1.4 us a stage
+// of 128 bytes and 11.5 us beside its stages (16 with the tanh GELU, 18.7 with
+// the erf form), a 128 x 256 half 0.8 and 9 (10.5 and 12).  The matrix pipe is
+// busy 64 % of the cycles at 2.0 GHz, without bank conflicts; 61 % in the 16-bit
+// kernel of the same bytes.  8192 rows, 16 groups, 4096 x 4096 157 us, with bias
+// and erf GELU 176, and 178 to 195 in a trace of single calls.
 #include "grouped16.hpp"
 #include "scaled.hpp"
 
@@ -30,9 +32,10 @@ __device__ __forceinline__ GemmArgs in_pairs(GemmArgs g)
 // matrix work, and a wavefront's sums, at most 128 registers, stay among the
 // 256 that vector instructions read.  With four wavefronts and sums in both
 // halves of the register file the compiler copies them back and forth in the
-// K loop, and without the copies one wavefront per SIMD is slower still
-// (4096 x 4096 x 4096: 62 us against 54; 8192 rows, 16 groups,
-// 4096 x 4096 with the copies 260 us a call, 203 with them suppressed).
+// K loop (8192 rows, 16 groups, 4096 x 4096: 260 us a call, 203 with the
+// copies suppressed), and without the copies one wavefront per SIMD was still
+// an eighth slower (4096 x 4096 x 4096, 62 us against 54 in the one run that
+// had both; this kernel's steady time is 57).
 template <int BM, int BN, int NS>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2)))
 void scaled_tile_kernel(ScaledArgs a)

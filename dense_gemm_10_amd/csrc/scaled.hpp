@@ -22,6 +22,9 @@ struct ScaledArgs {
     int32_t x_type;
 };
 
+// What a workgroup holds in registers while it makes the codes of few rows
+// (make_codes): 16 elements per thread of each row.  That all rows together
+// have no more is a choice (few_rows in scaled_api.cpp has the times).
 constexpr int kFewRows = 4;
 constexpr int64_t kFewElements = 8192;      // of all of them
 

@@ -41,11 +41,16 @@ bool is_noop(const dg_scaled_desc *d) { return d->groups == 0 || d->N == 0 || d-
 bool reads_ab(const dg_scaled_desc *d) { return d->alpha != 0.0f && d->K > 0; }
 
 // Few float rows, whose codes every workgroup of the product makes itself: no
-// workspace and no second launch (a 1 x 4096 x 4096 call takes the host 7.0 us
-// instead of 11.8 and the GPU, in a graph, 8.3 instead of 10.0; of more elements
-// the codes cost the workgroups more than they save: 4 x 16384 x 8192 35.8
-// against 31.8; and so they do in a layer of experts: 64 rows, 64 groups, 2048
-// x 2048 44.8 us a call against 35.6).
+// workspace and no second launch.  A 1 x 4096 x 4096 call takes the host 7.0 us
+// instead of 11.8.  On the GPU, in a graph, us against those of two launches,
+// rows x columns x K, up to the limits: 1 x 4096 x 4096 8.2 and 9.6, 1 x 4096 x
+// 8192 11.9 and 14.7, 1 x 16384 x 8192 29.7 and 31.7, 2 x 4096 x 4096 9.1 and
+// 9.5, 2 x 16384 x 4096 18.5 and 18.3; but 4 x 4096 x 2048 8.9 and 7.5, 4 x 16384
+// x 2048 14.7 and 12.7: of more than two rows only the shorter call wins.  Beyond
+// 8192 elements of one row a thread would hold more than 16; of all rows
+// together two launches win (4 x 16384 x 8192 35.8 against 31.8), and so they do
+// in a layer of experts (64 rows, 64 groups, 2048 x 2048 44.8 us a call against
+// 35.6).
 bool few_rows(const dg_scaled_desc *d)
 {
     return d->a_type != DG_I8 && d->groups == 1 && d->M <= DG_SCALED_FEW_ROWS && d->M * d->K <= DG_SCALED_FEW_ELEMENTS;
@@ -170,10 +175,11 @@ double expected_tiles(const dg_scaled_desc *d, int64_t bm, int64_t bn)
 //   128 x 128 with two stages and two workgroups (2000 rows, 16 groups, 4096 x
 //     2048 46.2 against 47.4 with four and 51.7);
 //   256 x 256, cut in halves where that saves a wave, from half a chip of
-//     them, with groups of 256 rows from a whole chip (2048 x 4096 x 4096 35.1
-//     against 36.4 on 128 x 128; 4096 x 4096 x 4096 56 against 70; 8192 rows,
-//     16 groups, 4096 x 4096 168 against 195; but 8192 rows, 8 groups, 1024 x
-//     4096, 144 of them, 61 against 59).
+//     them, with groups of 256 rows from a whole chip (2048 x 4096 x 4096 34.6
+//     against 36.2 on 128 x 128; 4096 x 4096 x 4096 57 against 70; 8192 rows,
+//     16 groups, 4096 x 4096 157 against 181, with bias and erf GELU 177 and
+//     198; of 8192 rows, 8 groups, 1024 x 4096, 144 of them, the lengths decide:
+//     61 against 59 with some, 48 against 55 with others).
 // Off the 16-byte grid, or with odd K: the same streaming kernels, then tiles
 // filled through registers, of 64 x 128 up to one per compute unit (64 x 4097 x
 // 1001 11.8 against 15.1 on 128 x 128, and 17 on 32 x 64 streamed; 300 x 4096 x

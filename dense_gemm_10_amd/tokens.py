@@ -322,9 +322,10 @@ def quantize_rows(x, place=None, q=None, scales=None, *, stream=None):
     NaN has scale NaN and codes 0.
 
     x: (tokens, width), row-major.  With ``place`` (of dispatch_tokens) token
-    t's codes and scale go to the rows place[t, j].  Returns (q, scales): int8
-    (rows, width), each row starting on 16 bytes if allocated here, and fp32
-    (rows,)."""
+    t's codes and scale go to the rows place[t, j], and rows that no slot has
+    keep what ``q`` and ``scales`` held (allocated here: nothing defined).
+    Returns (q, scales): int8 (rows, width), each row starting on 16 bytes if
+    allocated here, and fp32 (rows,)."""
     if stream is not None:
         return _there(stream, x, quantize_rows, x, place, q, scales)
     torch = _torch()

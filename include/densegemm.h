@@ -438,8 +438,9 @@ dg_status dg_gemm_qweight_describe(const dg_qweight_desc *d, char *buf, size_t l
  * and dweights 0 for a slot without; rows of dz that no slot has are left as
  * they were.  A place outside [0, rows) is one without a row, so no content
  * of the arrays makes a call read or write outside its operands.  Two slots
- * may have one row in dg_combine; in dg_spread and dg_combine_grad what that
- * row then gets is one of the two.
+ * may have one row in dg_combine; in dg_spread and dg_combine_grad each element
+ * of such a row then gets the value of either (dg_dispatch writes no such
+ * place).
  *
  * Types, ownership, streams and errors as in dg_gemm; no workspace, nothing
  * allocated, nothing read back; calls may be captured into HIP graphs.
@@ -502,9 +503,9 @@ dg_status dg_combine_grad(const dg_combine_desc *d, const void *dy, const void *
  * a row that holds an infinity or NaN gets scale NaN and codes 0.  With
  * `place` (tokens x top_k int32, packed, as dg_dispatch writes it) the codes
  * and scale of token t go to the rows place[t][j] of q and scales, in
- * [0, rows); other rows are left as they were, and a row that two tokens have
- * gets codes of either.  place NULL: row t, and rows
- * and top_k are ignored.
+ * [0, rows); other rows are left as they were.  Of a row that two tokens have,
+ * each code, and the scale, is of either, and codes and scale need not be of
+ * the same one.  place NULL: row t, and rows and top_k are ignored.
  *   x_type any dg_dtype; ldx, ldq >= max(1, width); tokens * top_k and rows
  *   at most 2^31 - 1. */
 typedef struct dg_quantize_desc {
